@@ -337,6 +337,106 @@ int vsa_kernels_per_run(void);
  * gave up. buf and status must be 16-byte aligned; bytes >= 16384. */
 vsa_status vsa_measure_l2_read(const void* buf, size_t bytes, int passes, int* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The projection side of the attention: what a transformer block computes
+ * between its hidden states and q, k, v. The pages describing the method have
+ * no counterpart of these entry points (their models bring their own).
+ * They keep no state and need no plan; the conventions above hold (16-byte
+ * aligned pointers, work only enqueued on `stream`), with strided tensors.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { VSA_TYPE_BF16 = 0, VSA_TYPE_FP16 = 1, VSA_TYPE_FP32 = 2 } vsa_type;
+
+/* A strided device tensor [B, heads, N, D] in the attention's index order,
+ * channels contiguous, strides in elements: s_b, s_h, s_n. It may be a view of
+ * a projection's output [B, N, heads, D] or a slice of a fused one. The
+ * strides of dimensions longer than 1 are multiples of 16 bytes; a written
+ * tensor's are not 0. */
+typedef struct {
+  void* data;
+  int heads;
+  long long s_b, s_h, s_n;
+} vsa_heads;
+
+#define VSA_ROPE_MAX_PAIRS 128
+#define VSA_ROPE_MAX_AXES 4
+
+/* Rotation of the leading `rot` channels of a head (even; 0 rotates none):
+ * pair j of them turns by pos[axis[j]] * freq[j] radians,
+ *   (u, v) -> (u cos - v sin, u sin + v cos).
+ * Pair j is channels (2j, 2j + 1) if interleaved, else (j, j + rot/2), and
+ * then rot is a multiple of 16. freq is rounded nowhere: angles are formed in
+ * double precision, so far positions lose nothing. */
+typedef struct {
+  int rot, interleaved;
+  int axes; /* 1 .. VSA_ROPE_MAX_AXES */
+  int axis[VSA_ROPE_MAX_PAIRS];
+  double freq[VSA_ROPE_MAX_PAIRS];
+} vsa_rotation;
+
+/* Positions of the tokens.
+ *   list == NULL: the raster grid, N = T*H*W, axes = 3, token (t, h, w) at
+ *     origin + (t, h, w) (an image has T = 1; a later frame of a video that is
+ *     generated frame by frame has T = 1 and its number in origin[0]).
+ *   list != NULL: device array [B, N, axes] of int32 (list_type 0) or fp32
+ *     (list_type 1), batches list_batch elements apart (0: one list for all). */
+typedef struct {
+  int T, H, W;
+  int origin[3];
+  const void* list;
+  int list_type;
+  long long list_batch;
+} vsa_positions;
+
+/* Sizes shared by q and k: type is a vsa_type; D a multiple of 8, at most 256.
+ * B, N or a tensor's heads may be 0 (nothing to do for it). */
+typedef struct {
+  int type;
+  int B, N, D;
+} vsa_rope_sizes;
+
+/* Rotary positions: q_out = R q and, where k and k_out are given, k_out = R k,
+ * which may have another number of heads. k and k_out may both be NULL. An
+ * output may be its own input (the same address and strides) and overlaps
+ * no other tensor of the call. */
+vsa_status vsa_rope(const vsa_rope_sizes* sizes, const vsa_rotation* rotation, const vsa_positions* positions,
+                    const vsa_heads* q, const vsa_heads* k, const vsa_heads* q_out, const vsa_heads* k_out,
+                    void* stream);
+
+/* Gradients of vsa_rope: the rotation by the opposite angles of dq_out (and
+ * dk_out) to dq (and dk). */
+vsa_status vsa_rope_backward(const vsa_rope_sizes* sizes, const vsa_rotation* rotation,
+                             const vsa_positions* positions, const vsa_heads* dq_out, const vsa_heads* dk_out,
+                             const vsa_heads* dq, const vsa_heads* dk, void* stream);
+
+/* RMS norm of every head's row and the rotation in one pass:
+ *   y = R (x w / sqrt(mean(x^2) + eps)),
+ * with w = q_weight for q and k_weight for k ([D] fp32, NULL for ones), eps >= 0.
+ * Sums and the norm are fp32; the result is rounded once. Otherwise as
+ * vsa_rope. */
+vsa_status vsa_qk_norm_rope(const vsa_rope_sizes* sizes, const vsa_rotation* rotation,
+                            const vsa_positions* positions, const vsa_heads* q, const vsa_heads* k,
+                            const float* q_weight, const float* k_weight, float eps, const vsa_heads* q_out,
+                            const vsa_heads* k_out, void* stream);
+
+/* Bytes of device workspace vsa_qk_norm_rope_backward needs on the current
+ * device for heads of D channels (0 if D is invalid or there is no sm_100
+ * device). */
+size_t vsa_qk_norm_rope_backward_workspace_bytes(int D);
+
+/* Gradients of vsa_qk_norm_rope, from its inputs q and k (the norm is
+ * recomputed from them; nothing is saved) and the gradients dq_out, dk_out of
+ * its outputs: dq, dk, and the weights' dq_weight, dk_weight ([D] fp32,
+ * written, summed over batches, heads and tokens in a fixed order; either may
+ * be NULL). dq may be q or dq_out itself, and so for k. The workspace
+ * is 16-byte aligned, the caller's, and used by one call at a time. */
+vsa_status vsa_qk_norm_rope_backward(const vsa_rope_sizes* sizes, const vsa_rotation* rotation,
+                                     const vsa_positions* positions, const vsa_heads* q, const vsa_heads* k,
+                                     const float* q_weight, const float* k_weight, float eps,
+                                     const vsa_heads* dq_out, const vsa_heads* dk_out, const vsa_heads* dq,
+                                     const vsa_heads* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

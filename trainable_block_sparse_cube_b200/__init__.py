@@ -5,7 +5,8 @@ The computation runs in libvsa.so (hand-written CUDA, C ABI in include/vsa.h);
 library; the first call does, and raises if it is not built or no sm_100
 GPU is present.
 """
-__all__ = ["Plan", "forward", "VSAError", "lib_path"]
+__all__ = ["Plan", "forward", "VSAError", "lib_path", "Rotation", "rope", "rope_backward", "qk_norm_rope",
+           "qk_norm_rope_backward"]
 
 
 def __getattr__(name):

@@ -10,7 +10,12 @@
 #include <new>
 
 #include "../../include/vsa.h"
+#include "host.cuh"
 #include "vsa_common.cuh"
+
+using vsa::aligned16;
+using vsa::EncodeTiledFn;
+using vsa::get_encode_fn;
 
 // State of vsa_run_host, created by its first call on a plan: device copies
 // of the inputs and results, a plan (and workspace) over one (batch, head)
@@ -58,23 +63,6 @@ struct vsa_plan_s {
 };
 
 namespace {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -163,8 +151,6 @@ void make_bwd_layout(const vsa_config* c, BwdLayout* L) {
   L->order_kv = take(BH * C * 4);
   L->total = off;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 2-D map over a cube-major copy: rows of D bf16, 64 x 64 boxes, 128-byte swizzle.
 vsa_status encode_cube_map(CUtensorMap* m, void* base, size_t rows, int D) {

@@ -1,0 +1,178 @@
+// Host side of the projection-side entry points of include/vsa.h (rotary
+// positions, per-head norm): argument checks and launches. They hold no state.
+#include <cmath>
+
+#include "host.cuh"
+#include "vsa_common.cuh"
+
+namespace {
+
+static_assert(vsa::kRopePairs == VSA_ROPE_MAX_PAIRS && vsa::kRopeAxes == VSA_ROPE_MAX_AXES, "ABI limits");
+
+// A strided [B, heads, N, D] tensor of `elem`-byte elements.
+vsa_status check_heads(const vsa_heads* x, int B, int N, int elem, bool written) {
+  if (x->heads < 0) return VSA_ERR_SHAPE;
+  if (x->heads > 65535) return VSA_ERR_UNSUPPORTED;
+  if (!B || !N || !x->heads) return VSA_OK;
+  if (!x->data) return VSA_ERR_INVALID_ARG;
+  if (!vsa::aligned16(x->data)) return VSA_ERR_ALIGN;
+  const int len[3] = {B, x->heads, N};
+  const long long stride[3] = {x->s_b, x->s_h, x->s_n};
+  for (int i = 0; i < 3; ++i)
+    if (len[i] > 1) {
+      if (stride[i] < 0 || (written && stride[i] == 0)) return VSA_ERR_INVALID_ARG;
+      if (stride[i] >= (1LL << 40)) return VSA_ERR_UNSUPPORTED;
+      if (stride[i] * elem % 16) return VSA_ERR_ALIGN;
+    }
+  return VSA_OK;
+}
+
+// The parts of RopeParams that every call shares.
+vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation* r, const vsa_positions* o) {
+  if (!s || !r || !o) return VSA_ERR_INVALID_ARG;
+  if (s->type < VSA_TYPE_BF16 || s->type > VSA_TYPE_FP32) return VSA_ERR_UNSUPPORTED;
+  if (s->B < 0 || s->N < 0) return VSA_ERR_SHAPE;
+  if (s->D < 8 || s->D > 256 || s->D % 8) return VSA_ERR_UNSUPPORTED;
+  if (s->B > (1 << 20)) return VSA_ERR_UNSUPPORTED;
+  if (r->rot < 0 || r->rot > s->D || r->rot % 2) return VSA_ERR_SHAPE;
+  if (!r->interleaved && r->rot % 16) return VSA_ERR_UNSUPPORTED;
+  if (r->axes < 1 || r->axes > VSA_ROPE_MAX_AXES) return VSA_ERR_UNSUPPORTED;
+  p->B = s->B;
+  p->N = s->N;
+  p->D = s->D;
+  p->rot = r->rot;
+  p->interleaved = r->interleaved != 0;
+  p->axes = r->axes;
+  for (int j = 0; j < r->rot / 2; ++j) {
+    if (r->axis[j] < 0 || r->axis[j] >= r->axes || !std::isfinite(r->freq[j])) return VSA_ERR_INVALID_ARG;
+    p->axis[j] = r->axis[j];
+    p->freq[j] = r->freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
+  }
+  if (!o->list) {
+    if (r->axes != 3 || o->T < 1 || o->H < 1 || o->W < 1) return VSA_ERR_SHAPE;
+    // each product stays below 2^62: no overflow
+    const long long hw = (long long)o->H * o->W;
+    if (s->N % hw || s->N / hw != o->T) return VSA_ERR_SHAPE;
+    p->pos_kind = 0;
+    p->H = o->H;
+    p->W = o->W;
+    for (int a = 0; a < 3; ++a) p->origin[a] = o->origin[a];
+  } else {
+    if (o->list_type != 0 && o->list_type != 1) return VSA_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(o->list) & 3u) return VSA_ERR_ALIGN;  // read element by element
+    if (o->list_batch < 0) return VSA_ERR_INVALID_ARG;
+    p->pos_kind = 1 + o->list_type;
+    p->pos = o->list;
+    p->pos_batch = o->list_batch;
+  }
+  return VSA_OK;
+}
+
+// One of q, k: its input, output and (norm backward) output gradient.
+vsa_status add_tensor(vsa::RopeParams* p, int t, int elem, const vsa_heads* in, const vsa_heads* dy,
+                      const vsa_heads* out, const float* w) {
+  if (!in && !out && !dy) return t ? VSA_OK : VSA_ERR_INVALID_ARG;
+  if (!in || !out) return VSA_ERR_INVALID_ARG;
+  if (in->heads != out->heads || (dy && dy->heads != in->heads)) return VSA_ERR_SHAPE;
+  vsa_status e = check_heads(in, p->B, p->N, elem, false);
+  if (e == VSA_OK && dy) e = check_heads(dy, p->B, p->N, elem, false);
+  if (e == VSA_OK) e = check_heads(out, p->B, p->N, elem, true);
+  if (e != VSA_OK) return e;
+  if (w && !vsa::aligned16(w)) return VSA_ERR_ALIGN;
+  vsa::RopeTensor& x = p->t[t];
+  x.in = in->data;
+  x.out = out->data;
+  x.w = w;
+  x.heads = in->heads;
+  x.in_b = in->s_b, x.in_h = in->s_h, x.in_n = in->s_n;
+  x.out_b = out->s_b, x.out_h = out->s_h, x.out_n = out->s_n;
+  if (dy) x.dy = dy->data, x.dy_b = dy->s_b, x.dy_h = dy->s_h, x.dy_n = dy->s_n;
+  return VSA_OK;
+}
+
+vsa_status run_rope(const vsa_rope_sizes* s, const vsa_rotation* r, const vsa_positions* o, const vsa_heads* q,
+                    const vsa_heads* k, const vsa_heads* q_out, const vsa_heads* k_out, bool back, bool norm,
+                    const float* wq, const float* wk, float eps, void* stream) {
+  vsa::RopeParams p{};
+  vsa_status e = fill(&p, s, r, o);
+  if (e != VSA_OK) return e;
+  if (norm && !(eps >= 0.f && std::isfinite(eps))) return VSA_ERR_INVALID_ARG;
+  const int elem = s->type == VSA_TYPE_FP32 ? 4 : 2;
+  e = add_tensor(&p, 0, elem, q, nullptr, q_out, wq);
+  if (e == VSA_OK) e = add_tensor(&p, 1, elem, k, nullptr, k_out, wk);
+  if (e != VSA_OK) return e;
+  if (!p.B || !p.N || !(p.t[0].heads + p.t[1].heads)) return VSA_OK;
+  int sms = 0;
+  e = vsa::current_device_sms(&sms);
+  if (e != VSA_OK) return e;
+  p.back = back;
+  p.norm = norm;
+  p.eps = eps;
+  return vsa::launch_rope(p, s->type, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+vsa_status vsa_rope(const vsa_rope_sizes* sizes, const vsa_rotation* rotation, const vsa_positions* positions,
+                    const vsa_heads* q, const vsa_heads* k, const vsa_heads* q_out, const vsa_heads* k_out,
+                    void* stream) {
+  return run_rope(sizes, rotation, positions, q, k, q_out, k_out, false, false, nullptr, nullptr, 0.f, stream);
+}
+
+vsa_status vsa_rope_backward(const vsa_rope_sizes* sizes, const vsa_rotation* rotation,
+                             const vsa_positions* positions, const vsa_heads* dq_out, const vsa_heads* dk_out,
+                             const vsa_heads* dq, const vsa_heads* dk, void* stream) {
+  return run_rope(sizes, rotation, positions, dq_out, dk_out, dq, dk, true, false, nullptr, nullptr, 0.f, stream);
+}
+
+vsa_status vsa_qk_norm_rope(const vsa_rope_sizes* sizes, const vsa_rotation* rotation,
+                            const vsa_positions* positions, const vsa_heads* q, const vsa_heads* k,
+                            const float* q_weight, const float* k_weight, float eps, const vsa_heads* q_out,
+                            const vsa_heads* k_out, void* stream) {
+  return run_rope(sizes, rotation, positions, q, k, q_out, k_out, false, true, q_weight, k_weight, eps, stream);
+}
+
+size_t vsa_qk_norm_rope_backward_workspace_bytes(int D) {
+  int sms = 0;
+  if (D < 8 || D > 256 || D % 8 || vsa::current_device_sms(&sms) != VSA_OK) return 0;
+  return vsa::norm_rope_partial_bytes(D, sms);
+}
+
+vsa_status vsa_qk_norm_rope_backward(const vsa_rope_sizes* sizes, const vsa_rotation* rotation,
+                                     const vsa_positions* positions, const vsa_heads* q, const vsa_heads* k,
+                                     const float* q_weight, const float* k_weight, float eps,
+                                     const vsa_heads* dq_out, const vsa_heads* dk_out, const vsa_heads* dq,
+                                     const vsa_heads* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t ws_bytes, void* stream) {
+  vsa::RopeParams p{};
+  vsa_status e = fill(&p, sizes, rotation, positions);
+  if (e != VSA_OK) return e;
+  if (!(eps >= 0.f && std::isfinite(eps)) || !dq_out || (k && !dk_out)) return VSA_ERR_INVALID_ARG;
+  const int elem = sizes->type == VSA_TYPE_FP32 ? 4 : 2;
+  e = add_tensor(&p, 0, elem, q, dq_out, dq, q_weight);
+  if (e == VSA_OK) e = add_tensor(&p, 1, elem, k, dk_out, dk, k_weight);
+  if (e != VSA_OK) return e;
+  if ((dq_weight && !vsa::aligned16(dq_weight)) || (dk_weight && !vsa::aligned16(dk_weight))) return VSA_ERR_ALIGN;
+  int sms = 0;
+  e = vsa::current_device_sms(&sms);
+  if (e != VSA_OK) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!p.B || !p.N || !(p.t[0].heads + p.t[1].heads)) {  // no rows: the sums are 0
+    for (float* dw : {dq_weight, dk_weight})
+      if (dw && cudaMemsetAsync(dw, 0, (size_t)p.D * 4, st) != cudaSuccess) return VSA_ERR_CUDA;
+    return VSA_OK;
+  }
+  if (!workspace) return VSA_ERR_INVALID_ARG;
+  if (!vsa::aligned16(workspace)) return VSA_ERR_ALIGN;
+  if (ws_bytes < vsa::norm_rope_partial_bytes(p.D, sms)) return VSA_ERR_INVALID_ARG;
+  p.back = 1;
+  p.norm = 1;
+  p.eps = eps;
+  p.partial = static_cast<float*>(workspace);
+  return vsa::launch_norm_rope_backward(p, sizes->type, dq_weight, dk_weight, sms, st) == cudaSuccess ? VSA_OK
+                                                                                                      : VSA_ERR_CUDA;
+}
+
+}  // extern "C"

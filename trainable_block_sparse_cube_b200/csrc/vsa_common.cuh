@@ -153,6 +153,42 @@ struct BwdFineParams {
   float scale;           // 1 / sqrt(D)
 };
 
+// ---------------------------------------------------------------- rotary positions, norm
+constexpr int kRopeAxes = 4, kRopePairs = 128;
+
+// q or k of a rotation: strided views [B, heads, N, D] (element strides, channels contiguous).
+struct RopeTensor {
+  const void* in;
+  const void* dy;      // norm backward: gradient of the output
+  void* out;
+  const float* w;      // norm weight [D] or null (ones)
+  int heads;           // 0: no such tensor
+  long long in_b, in_h, in_n, dy_b, dy_h, dy_n, out_b, out_h, out_n;
+};
+
+struct RopeParams {
+  RopeTensor t[2];          // q, k
+  int B, N, D;
+  int rot, interleaved;     // rotated leading channels; pairs (2i, 2i + 1) or (i, i + rot/2)
+  int axes;
+  double freq[kRopePairs];  // turns (radians / 2 pi) per unit of position
+  int axis[kRopePairs];
+  int pos_kind;             // 0: raster grid of H x W frames; 1: int32 list; 2: fp32 list
+  int H, W, origin[3];
+  const void* pos;          // list [B or 1, N, axes]
+  long long pos_batch;      // elements between batches of the list (0: one list for all)
+  int back;                 // rotate by the opposite angle
+  int norm;
+  float eps;
+  float* partial;           // norm backward: [grid, 2, D] weight gradients of the blocks
+  int tiles, groups;        // work split, set by the launcher
+  long long units;
+};
+
+cudaError_t launch_rope(RopeParams p, int type, int num_sms, cudaStream_t st);
+size_t norm_rope_partial_bytes(int D, int num_sms);
+cudaError_t launch_norm_rope_backward(RopeParams p, int type, float* dwq, float* dwk, int num_sms, cudaStream_t st);
+
 cudaError_t launch_gather(const GatherParams& p, int D, int num_sms, cudaStream_t st);
 cudaError_t launch_coarse(const CoarseParams& p, cudaStream_t st);
 cudaError_t launch_fine(const FineParams& p, int D, int grid, cudaStream_t st);

@@ -23,7 +23,12 @@ EXPORTED = ["vsa_workspace_bytes", "vsa_workspace_layout", "vsa_plan", "vsa_run"
             "vsa_set_debug_stall", "vsa_set_stage_timing", "vsa_stage_times", "vsa_kernels_per_run",
             "vsa_forward_noalloc", "vsa_set_cube_major_copies", "vsa_run_host", "vsa_measure_l2_read",
             "vsa_run_train", "vsa_backward_workspace_bytes", "vsa_run_backward", "vsa_backward_stage_times",
-            "vsa_stage_times_history", "vsa_backward_stage_times_history"]
+            "vsa_stage_times_history", "vsa_backward_stage_times_history",
+            "vsa_rope", "vsa_rope_backward", "vsa_qk_norm_rope", "vsa_qk_norm_rope_backward_workspace_bytes",
+            "vsa_qk_norm_rope_backward"]
+
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ROPE_MAX_PAIRS, ROPE_MAX_AXES = 128, 4
 
 
 class VSAError(RuntimeError):
@@ -42,6 +47,25 @@ class WorkspaceLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("q_cube", "k_cube", "v_cube", "q_pool", "k_pool", "v_pool",
                                                "o_coarse", "s_coarse", "pool_split", "p_split", "cnt", "order",
                                                "err", "total")]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int), ("s_b", ctypes.c_longlong),
+                ("s_h", ctypes.c_longlong), ("s_n", ctypes.c_longlong)]
+
+
+class RotationSpec(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("axes", ctypes.c_int),
+                ("axis", ctypes.c_int * ROPE_MAX_PAIRS), ("freq", ctypes.c_double * ROPE_MAX_PAIRS)]
+
+
+class Positions(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("W", ctypes.c_int), ("origin", ctypes.c_int * 3),
+                ("list", ctypes.c_void_p), ("list_type", ctypes.c_int), ("list_batch", ctypes.c_longlong)]
+
+
+class RopeSizes(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("B", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int)]
 
 
 _lib = None
@@ -104,6 +128,18 @@ def load():
     L.vsa_backward_stage_times_history.restype = i32
     L.vsa_measure_l2_read.argtypes = [vp, sz, i32, vp, vp]
     L.vsa_measure_l2_read.restype = i32
+    H, F = ctypes.POINTER(Heads), ctypes.POINTER
+    what = [F(RopeSizes), F(RotationSpec), F(Positions)]
+    L.vsa_rope.argtypes = what + [H] * 4 + [vp]
+    L.vsa_rope.restype = i32
+    L.vsa_rope_backward.argtypes = what + [H] * 4 + [vp]
+    L.vsa_rope_backward.restype = i32
+    L.vsa_qk_norm_rope.argtypes = what + [H, H, vp, vp, ctypes.c_float, H, H, vp]
+    L.vsa_qk_norm_rope.restype = i32
+    L.vsa_qk_norm_rope_backward_workspace_bytes.argtypes = [i32]
+    L.vsa_qk_norm_rope_backward_workspace_bytes.restype = sz
+    L.vsa_qk_norm_rope_backward.argtypes = what + [H, H, vp, vp, ctypes.c_float, H, H, H, H, vp, vp, vp, sz, vp]
+    L.vsa_qk_norm_rope_backward.restype = i32
     _lib = L
     return L
 
@@ -352,3 +388,207 @@ def forward(q, k, v, gate_c, gate_f, T, H, W, topk=0, top_p=0.0, out=None, idx=N
     _check(load().vsa_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(gate_c), _ptr(gate_f), B, heads, T, H, W, D, topk,
                               ctypes.c_float(top_p), _ptr(out), _ptr(idx), _stream()), "vsa_forward")
     return out, idx
+
+
+# ---------------------------------------------------------------- the projection side
+class Rotation:
+    """How the channels of a head turn with a token's positions.
+
+    ``sections``: rotated channels of each axis (even; one to four axes, in
+    order; together at most D, the remaining channels are not rotated). Pair i
+    of an axis' n channels turns by position * scale * base**(-2i/n); with
+    ``shared`` the pairs of all axes are numbered through and share one table,
+    base**(-2j/sum). ``scale``: factor on each axis' positions (default 1).
+    Pairs are channels (2j, 2j+1) if ``interleaved``, else (j, j + rot/2) of the
+    rot = sum(sections) rotated channels, and then rot is a multiple of 16.
+    """
+
+    def __init__(self, D, sections, base=10000.0, scale=None, interleaved=True, shared=False):
+        self.D, self.sections = int(D), tuple(int(n) for n in sections)
+        self.interleaved, self.axes, self.rot = bool(interleaved), len(self.sections), sum(self.sections)
+        if not 1 <= self.axes <= ROPE_MAX_AXES or any(n < 0 or n % 2 for n in self.sections):
+            raise ValueError(f"sections must be one to {ROPE_MAX_AXES} even numbers, got {self.sections}")
+        if not 0 <= self.rot <= min(self.D, 2 * ROPE_MAX_PAIRS):
+            raise ValueError(f"sections {self.sections} do not fit into {self.D} channels")
+        if not self.interleaved and self.rot % 16:
+            raise ValueError("pairs (j, j + rot/2) need sections that add up to a multiple of 16")
+        if not base > 0:
+            raise ValueError("base must be positive")
+        scale = (1.0,) * self.axes if scale is None else tuple(float(x) for x in scale)
+        if len(scale) != self.axes:
+            raise ValueError("scale must have one factor for each axis")
+        self.spec = RotationSpec(self.rot, int(self.interleaved), self.axes)
+        j = 0
+        for a, n in enumerate(self.sections):
+            for i in range(n // 2):
+                self.spec.axis[j] = a
+                self.spec.freq[j] = scale[a] * float(base) ** (-2.0 * j / self.rot if shared else -2.0 * i / n)
+                j += 1
+
+
+class _OnDevice:
+    """Makes the tensors' device current for the length of a call."""
+
+    def __init__(self, device):
+        self.device, self.before = device.index, None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.device:
+            self.before = now
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+
+def _need_heads(t, name, like=None, dtype=None, device=None):
+    """A CUDA tensor [B, heads, N, D] of any strides whose channels are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have shape [B, heads, N, D], got {tuple(t.shape)}")
+    if t.dtype not in TYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if like is not None and t.shape != like:
+        raise ValueError(f"{name} must have shape {tuple(like)}, got {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+
+
+def _heads(t):
+    return None if t is None else ctypes.byref(Heads(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1), t.stride(2)))
+
+
+def _where(rotation, grid, origin, positions, B, N, device):
+    if (grid is None) == (positions is None):
+        raise ValueError("give either grid or positions")
+    if grid is not None:
+        if rotation.axes != 3 or len(grid) != 3 or len(origin) != 3:
+            raise ValueError("a grid and its origin have three numbers (T, H, W), and the rotation three axes")
+        if any(not -2 ** 31 <= o < 2 ** 31 for o in origin):
+            raise ValueError("origin must fit into 32 bits")
+        if N != grid[0] * grid[1] * grid[2]:
+            raise ValueError(f"N = {N} must equal T*H*W of grid {tuple(grid)}")
+        return Positions(grid[0], grid[1], grid[2], (ctypes.c_int * 3)(*origin), None, 0, 0)
+    p = positions
+    if not isinstance(p, torch.Tensor) or not p.is_cuda or p.device != device:
+        raise ValueError(f"positions must be a CUDA tensor on {device}")
+    if p.dtype not in (torch.int32, torch.float32):
+        raise ValueError(f"positions must be int32 or float32, got {p.dtype}")
+    if p.dim() == 2:
+        p = p[None]
+    if tuple(p.shape) not in ((B, N, rotation.axes), (1, N, rotation.axes)):
+        raise ValueError(f"positions must have shape [{N}, {rotation.axes}] or [{B}, {N}, {rotation.axes}], "
+                         f"got {tuple(positions.shape)}")
+    if p.numel() and not p[0].is_contiguous():
+        raise ValueError("positions must be contiguous")
+    return Positions(0, 0, 0, (ctypes.c_int * 3)(), p.data_ptr() if p.numel() else 16,
+                     0 if p.dtype == torch.int32 else 1, p.stride(0) if p.shape[0] > 1 else 0)
+
+
+def _sizes(q, k, rotation, names=("q", "k")):
+    _need_heads(q, names[0])
+    B, _, N, D = q.shape
+    if rotation.D != D:
+        raise ValueError(f"the rotation is for {rotation.D} channels, {names[0]} has {D}")
+    if k is not None:
+        _need_heads(k, names[1], dtype=q.dtype, device=q.device)
+        if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, D):
+            raise ValueError(f"{names[1]} must have shape [{B}, heads, {N}, {D}], got {tuple(k.shape)}")
+    return RopeSizes(TYPES[q.dtype], B, N, D)
+
+
+def _need_weight(w, name, D, device):
+    if w is not None:
+        _need(w, name, torch.float32, (D,))
+        if w.device != device:
+            raise ValueError(f"{name} is on {w.device}, not {device}")
+
+
+def _outputs(q, k, q_out, k_out, names, like_input=False):
+    """The given outputs, checked, or new ones: contiguous, or in the inputs' order of dimensions."""
+    out = []
+    for t, o, name in ((q, q_out, names[0]), (k, k_out, names[1])):
+        if t is None:
+            if o is not None:
+                raise ValueError(f"{name} has no input")
+        elif o is None:
+            o = torch.empty_like(t) if like_input else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        else:
+            _need_heads(o, name, like=t.shape, dtype=t.dtype, device=t.device)
+        out.append(o)
+    return out
+
+
+def rope(q, k, rotation, grid=None, origin=(0, 0, 0), positions=None, q_out=None, k_out=None):
+    """Rotary positions with several axes on q and k ([B, heads, N, D], any strides; k may be None or have
+    another number of heads). Tokens lie on the raster ``grid`` (T, H, W) from ``origin`` on, or at
+    ``positions`` ([N, axes] or [B, N, axes], int32 or float32). Returns (q_out, k_out), contiguous unless
+    given; an output may be its input. Enqueued on the current stream."""
+    sizes = _sizes(q, k, rotation)
+    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, q.device)
+    with _OnDevice(q.device):
+        q_out, k_out = _outputs(q, k, q_out, k_out, ("q_out", "k_out"))
+        _check(load().vsa_rope(sizes, rotation.spec, where, _heads(q), _heads(k), _heads(q_out), _heads(k_out),
+                               _stream()), "vsa_rope")
+    return q_out, k_out
+
+
+def rope_backward(dq_out, dk_out, rotation, grid=None, origin=(0, 0, 0), positions=None, dq=None, dk=None):
+    """Gradients of rope's inputs from those of its outputs (dk_out may be None): (dq, dk), contiguous unless
+    given. Enqueued on the current stream."""
+    sizes = _sizes(dq_out, dk_out, rotation, ("dq_out", "dk_out"))
+    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, dq_out.device)
+    with _OnDevice(dq_out.device):
+        dq, dk = _outputs(dq_out, dk_out, dq, dk, ("dq", "dk"))
+        _check(load().vsa_rope_backward(sizes, rotation.spec, where, _heads(dq_out), _heads(dk_out), _heads(dq),
+                                        _heads(dk), _stream()), "vsa_rope_backward")
+    return dq, dk
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, rotation, grid=None, origin=(0, 0, 0), positions=None, eps=1e-6,
+                 q_out=None, k_out=None):
+    """RMS norm of every head's queries and keys (weights [D] fp32 or None) and the rotation of ``rope`` in one
+    pass; arguments, outputs and stream as there."""
+    sizes = _sizes(q, k, rotation)
+    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, q.device)
+    _need_weight(q_weight, "q_weight", sizes.D, q.device)
+    _need_weight(k_weight, "k_weight", sizes.D, q.device)
+    with _OnDevice(q.device):
+        q_out, k_out = _outputs(q, k, q_out, k_out, ("q_out", "k_out"))
+        _check(load().vsa_qk_norm_rope(sizes, rotation.spec, where, _heads(q), _heads(k), _ptr(q_weight),
+                                       _ptr(k_weight), eps, _heads(q_out), _heads(k_out), _stream()),
+               "vsa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, rotation, grid=None, origin=(0, 0, 0),
+                          positions=None, eps=1e-6, dq=None, dk=None):
+    """Gradients of qk_norm_rope from its inputs (nothing is saved) and the gradients of its outputs. Returns
+    (dq, dk, dq_weight, dk_weight): dq and dk in the order of dimensions that q and k are stored in unless
+    given, the weights' in fp32 (None where the weight is None). Enqueued on the current stream."""
+    sizes = _sizes(q, k, rotation)
+    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, q.device)
+    _need_weight(q_weight, "q_weight", sizes.D, q.device)
+    _need_weight(k_weight, "k_weight", sizes.D, q.device)
+    _need_heads(dq_out, "dq_out", like=q.shape, dtype=q.dtype, device=q.device)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out must be given together")
+    if k is not None:
+        _need_heads(dk_out, "dk_out", like=k.shape, dtype=q.dtype, device=q.device)
+    with _OnDevice(q.device):
+        L = load()
+        dq, dk = _outputs(q, k, dq, dk, ("dq", "dk"), like_input=True)
+        dwq = None if q_weight is None else torch.empty_like(q_weight)
+        dwk = None if k is None or k_weight is None else torch.empty_like(k_weight)
+        nb = L.vsa_qk_norm_rope_backward_workspace_bytes(sizes.D)
+        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        _check(L.vsa_qk_norm_rope_backward(sizes, rotation.spec, where, _heads(q), _heads(k), _ptr(q_weight),
+                                           _ptr(k_weight), eps, _heads(dq_out), _heads(dk_out), _heads(dq), _heads(dk),
+                                           _ptr(dwq), _ptr(dwk), _ptr(ws), nb, _stream()),
+               "vsa_qk_norm_rope_backward")
+    return dq, dk, dwq, dwk
