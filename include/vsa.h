@@ -437,6 +437,63 @@ vsa_status vsa_qk_norm_rope_backward(const vsa_rope_sizes* sizes, const vsa_rota
                                      const vsa_heads* dk, float* dq_weight, float* dk_weight, void* workspace,
                                      size_t ws_bytes, void* stream);
 
+/* Linear product and its gradients: the projections into and out of the
+ * attention and the feed-forward's,
+ *   y = act(x W^T + bias) + residual.
+ * x, y and what has their shape are vsa_heads views of B x N rows: a tensor
+ * [B, N, channels] has one head, one in the attention's layout [B, heads, N, D]
+ * is rows of heads * D channels, channel h * D + d first in head order. With
+ * more than one head D is a multiple of 64. W is [F, K], its rows
+ * weight_stride elements apart. K and F are multiples of 8; type is
+ * VSA_TYPE_BF16 or VSA_TYPE_FP16, of every tensor but bias and dbias (fp32).
+ * Sums are fp32 and the results rounded once. B or N may be 0. */
+typedef struct {
+  int type;
+  int B, N, K, F;
+} vsa_linear_sizes;
+
+typedef enum {
+  VSA_ACT_NONE = 0,
+  VSA_ACT_SILU = 1,
+  VSA_ACT_GELU = 2,     /* z times the normal distribution function */
+  VSA_ACT_GELU_TANH = 3 /* its tanh form */
+} vsa_activation;
+
+/* Bytes of device workspace vsa_linear needs at most for these sizes on the
+ * current device (often 0; 0 too if they are invalid). */
+size_t vsa_linear_workspace_bytes(const vsa_linear_sizes* sizes);
+
+/* y to `out`. bias ([F]), residual and z may be NULL; residual and z have as
+ * many heads as out; z receives x W^T + bias for vsa_linear_backward. out may
+ * be the residual itself and overlaps no other tensor of the call. The
+ * workspace is used by one call at a time. */
+vsa_status vsa_linear(const vsa_linear_sizes* sizes, const vsa_heads* x, const void* weight, long long weight_stride,
+                      const float* bias, int activation, const vsa_heads* residual, const vsa_heads* z,
+                      const vsa_heads* out, void* workspace, size_t ws_bytes, void* stream);
+
+size_t vsa_linear_backward_workspace_bytes(const vsa_linear_sizes* sizes, int activation);
+
+/* Gradients from that of the output, with dz = dout act'(z):
+ *   dx = dz W,  dweight [F, K] = dz^T x,  dbias [F] (fp32) = sum of dz over rows;
+ * the residual's gradient is dout. Any of dx, dweight and dbias may be NULL. x
+ * is read for dweight, the weight for dx, z (as many heads as dout) with an
+ * activation. dz is rounded to the type before its products, not for dbias.
+ * Sums run in a fixed order. */
+vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x, const void* weight,
+                               long long weight_stride, const vsa_heads* z, int activation, const vsa_heads* dout,
+                               const vsa_heads* dx, void* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* Synchronises `stream` and returns VSA_ERR_TIMEOUT if a wait inside a linear
+ * product of the current device gave up since the last check (its results are
+ * then invalid). Not while a graph is captured. */
+vsa_status vsa_linear_check(void* stream);
+
+/* Test hook, for all calls of the process: the limit of the linear product's
+ * device-side waits (1 s by default), and whether its operands are left
+ * unloaded so that the waits run out. */
+vsa_status vsa_linear_set_limits(uint64_t wait_ns, int stall);
+
 #ifdef __cplusplus
 }
 #endif

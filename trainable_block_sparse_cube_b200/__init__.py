@@ -6,7 +6,7 @@ library; the first call does, and raises if it is not built or no sm_100
 GPU is present.
 """
 __all__ = ["Plan", "forward", "VSAError", "lib_path", "Rotation", "rope", "rope_backward", "qk_norm_rope",
-           "qk_norm_rope_backward"]
+           "qk_norm_rope_backward", "linear", "linear_backward", "linear_check"]
 
 
 def __getattr__(name):

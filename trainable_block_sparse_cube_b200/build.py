@@ -10,7 +10,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC = ["api.cu", "gather.cu", "coarse.cu", "fine.cu", "measure.cu", "backward.cu", "fine_bwd.cu", "schedule.cu",
-       "rope.cu", "api_project.cu"]
+       "rope.cu", "api_project.cu", "linear.cu", "api_linear.cu"]
 LIB = os.path.join(HERE, "libvsa.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -29,7 +29,7 @@ def _nvcc() -> str:
 
 def build(verbose: bool = False, force: bool = False) -> str:
     srcs = [os.path.join(HERE, "csrc", s) for s in SRC]
-    deps = srcs + [os.path.join(HERE, "csrc", h) for h in ("vsa_common.cuh", "sm100_ptx.cuh", "host.cuh")]
+    deps = srcs + [os.path.join(HERE, "csrc", h) for h in ("vsa_common.cuh", "sm100_ptx.cuh", "pair_ptx.cuh", "host.cuh")]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "vsa.h"))
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)

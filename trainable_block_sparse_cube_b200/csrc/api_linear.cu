@@ -1,0 +1,442 @@
+// Host side of the linear product's entry points of include/vsa.h: argument
+// checks, the choice of tiles, tensor maps and launches.
+#include <atomic>
+
+#include "host.cuh"
+#include "vsa_common.cuh"
+
+namespace {
+
+using vsa::RowsView;
+
+std::atomic<unsigned long long> g_wait_ns{1000000000ull};
+std::atomic<int> g_stall{0};
+
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// How a product of `batches` x `rows` x `cols` over `kblocks` 64-long steps is cut.
+struct Tiling {
+  int bn, splits;
+};
+
+// The pairs run in rounds; a round costs its steps (the MMA of a step takes
+// 2 bn cycles, its loads 16 + bn/16 KB at the 47 bytes a cycle that an SM gets
+// of the L2's rate) plus the start and the epilogue of a tile, and a split
+// contraction a second kernel that reads the parts again. bn = 192 fills the
+// last round where 256 leaves it short; `wide` excludes it where a tile's
+// second half would start inside a head.
+Tiling choose(long long batches, long long rows, long long cols, long long kblocks, int sms, bool wide) {
+  const long long pairs = sms / 2;
+  Tiling best{256, 1};
+  double best_cost = -1;
+  for (int bn : {256, 192, 128}) {
+    if (wide && bn == 192) continue;
+    const long long tiles = batches * ceil_div(rows, 256) * ceil_div(cols, bn);
+    const double load = (16384 + 64.0 * bn) / 47, step = load > 2.0 * bn ? load : 2.0 * bn;
+    for (int s = 1; s <= 32 && s <= kblocks; ++s) {
+      if (s > 1 && tiles * (s - 1) >= pairs) break;  // every pair has work already
+      const long long rounds = ceil_div(tiles * s, pairs);
+      double cost = rounds * (ceil_div(kblocks, s) * step + 800) + 12.0 * bn;
+      if (s > 1) cost += 5000 + 8.0 * s * batches * rows * cols / 2700;
+      if (best_cost < 0 || cost < best_cost) best_cost = cost, best = Tiling{bn, s};
+    }
+  }
+  return best;
+}
+
+// One product: what a tile needs to know, and the bytes of its parts.
+struct Product {
+  int kind;
+  long long batches, rows, cols, kblocks, kblocks_batch;
+  bool wide;
+  Tiling t;
+
+  void plan(int sms) { t = choose(batches, rows, cols, kblocks, sms, wide); }
+  size_t partial_bytes() const { return t.splits > 1 ? align_up((size_t)t.splits * batches * rows * cols * 4) : 0; }
+};
+
+// The batches of a call are one run of rows if every view allows it.
+bool joined(int B, int N, std::initializer_list<const vsa_heads*> views) {
+  if (B == 1) return true;
+  for (const vsa_heads* v : views)
+    if (v && v->s_b != (long long)N * v->s_n) return false;
+  return true;
+}
+
+Product forward_product(const vsa_linear_sizes* s, bool join) {
+  Product p{};
+  p.kind = vsa::kGemmForward;
+  p.batches = join ? 1 : s->B;
+  p.rows = join ? (long long)s->B * s->N : s->N;
+  p.cols = s->F;
+  p.kblocks = ceil_div(s->K, 64);
+  return p;
+}
+Product input_product(const vsa_linear_sizes* s, bool join) {
+  Product p = forward_product(s, join);
+  p.kind = vsa::kGemmInput;
+  p.cols = s->K;
+  p.kblocks = ceil_div(s->F, 64);
+  return p;
+}
+Product weight_product(const vsa_linear_sizes* s, bool join, bool wide) {
+  Product p{};
+  p.kind = vsa::kGemmWeight;
+  p.batches = 1;
+  p.rows = s->F;
+  p.cols = s->K;
+  p.kblocks_batch = ceil_div(join ? (long long)s->B * s->N : s->N, 64);
+  p.kblocks = p.kblocks_batch * (join ? 1 : s->B);
+  p.wide = wide;
+  return p;
+}
+
+bool skinny(const vsa_linear_sizes* s) { return (long long)s->B * s->N <= vsa::kSkinnyRows; }
+
+int slope_blocks(long long M, int F, int sms) {
+  const long long strips = ceil_div(F, 256), rows = ceil_div(M, 8), most = 8LL * sms / strips;
+  return (int)(rows < most ? rows : most > 1 ? most : 1);
+}
+
+vsa_status check_sizes(const vsa_linear_sizes* s) {
+  if (!s) return VSA_ERR_INVALID_ARG;
+  if (s->type != VSA_TYPE_BF16 && s->type != VSA_TYPE_FP16) return VSA_ERR_UNSUPPORTED;
+  if (s->B < 0 || s->N < 0 || s->K < 1 || s->F < 1) return VSA_ERR_SHAPE;
+  if (s->K % 8 || s->F % 8 || s->K > (1 << 20) || s->F > (1 << 20) || s->B > (1 << 20)) return VSA_ERR_UNSUPPORTED;
+  if ((long long)s->B * s->N > (1LL << 30)) return VSA_ERR_UNSUPPORTED;
+  return VSA_OK;
+}
+
+// A view of B x N rows of `channels`. With several heads a 64-long step must not cross one.
+vsa_status check_view(const vsa_heads* v, const vsa_linear_sizes* s, int channels, bool written) {
+  if (!v) return VSA_ERR_INVALID_ARG;
+  if (v->heads < 1 || channels % v->heads) return VSA_ERR_SHAPE;
+  if (v->heads > 1 && channels / v->heads % 64) return VSA_ERR_UNSUPPORTED;
+  vsa_status e = vsa::check_heads(v, s->B, s->N, 2, written);
+  if (e != VSA_OK) return e;
+  for (long long st : {s->B > 1 ? v->s_b : 0, v->heads > 1 ? v->s_h : 0, s->N > 1 ? v->s_n : 0})
+    if (st >= (1LL << 38)) return VSA_ERR_UNSUPPORTED;  // the tensor maps' limit is 2^40 bytes
+  return VSA_OK;
+}
+
+// One token a batch: the batches are the rows. Returns the view to use, a copy in *store if it differs.
+const vsa_heads* single_token(const vsa_heads* v, bool swap, vsa_heads* store) {
+  if (!v || !swap) return v;
+  *store = *v;
+  store->s_n = v->s_b;
+  store->s_b = 0;
+  return store;
+}
+
+RowsView rows_view(const vsa_heads* v, int channels) {
+  return v ? RowsView{v->data, v->heads, channels / v->heads, v->s_b, v->s_h, v->s_n} : RowsView{};
+}
+RowsView plain_rows(void* data, long long N, int channels) {
+  return RowsView{data, 1, channels, N * channels, channels, channels};
+}
+
+// 4-D map (channel of a head, row, head, batch), 128-byte swizzle.
+vsa_status encode(CUtensorMap* m, const RowsView& v, long long rows, long long batches, int box_rows, int type,
+                  bool fp32 = false) {
+  vsa::EncodeTiledFn enc = vsa::get_encode_fn();
+  if (!enc) return VSA_ERR_CUDA;
+  const int elem = fp32 ? 4 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)v.D, (cuuint64_t)rows, (cuuint64_t)v.heads, (cuuint64_t)batches};
+  // strides of dimensions of length 1 are not used, but have to be valid
+  const cuuint64_t row = (cuuint64_t)v.D * elem;
+  const cuuint64_t strides[3] = {rows > 1 ? (cuuint64_t)v.s_n * elem : row, v.heads > 1 ? (cuuint64_t)v.s_h * elem : row,
+                                 batches > 1 ? (cuuint64_t)v.s_b * elem : row};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType dt = fp32      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : type    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(m, dt, 4, v.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? VSA_OK
+             : VSA_ERR_CUDA;
+}
+
+struct Epilogue {
+  const float* bias;
+  int act;
+  RowsView residual, z, out;
+};
+
+// out = epilogue(A B): A has rows (or, for the weights' gradient, columns of a
+// run of rows) of `a`, B those of `b`. `b_rows`: rows of b's map.
+vsa_status run_product(const Product& p, int type, const RowsView& a, const RowsView& b, long long b_rows,
+                       const Epilogue& ep, void* workspace, int sms, cudaStream_t st) {
+  vsa::GemmParams g{};
+  const bool weight = p.kind == vsa::kGemmWeight;
+  const long long runs = weight ? p.kblocks / p.kblocks_batch : p.batches, run_rows = weight ? b_rows : p.rows;
+  const int half = p.t.bn / 2;
+  vsa_status e = encode(&g.ta, a, run_rows, runs, weight ? 64 : 128, type);
+  if (e == VSA_OK) e = encode(&g.tb, b, b_rows, weight ? runs : 1, p.kind == vsa::kGemmForward ? half : 64, type);
+  const bool split = p.t.splits > 1;
+  if (e == VSA_OK) {
+    if (split) {
+      RowsView parts{workspace, (int)p.batches, (int)p.cols, (long long)p.batches * p.rows * p.cols,
+                     (long long)p.rows * p.cols, p.cols};
+      e = encode(&g.tout, parts, p.rows, p.t.splits, 32, type, true);
+    } else {
+      e = encode(&g.tout, ep.out, p.rows, p.batches, 32, type);
+      if (e == VSA_OK && ep.residual.data) e = encode(&g.tres, ep.residual, p.rows, p.batches, 32, type);
+      if (e == VSA_OK && ep.z.data) e = encode(&g.tz, ep.z, p.rows, p.batches, 32, type);
+    }
+  }
+  if (e != VSA_OK) return e;
+  g.a_d = a.D;
+  g.b_d = b.D;
+  g.o_d = ep.out.D;
+  g.bn = p.t.bn;
+  g.batches = (int)p.batches;
+  g.rows = (int)p.rows;
+  g.row_tiles = (int)ceil_div(p.rows, 256);
+  g.F = (int)p.cols;
+  g.col_tiles = (int)ceil_div(p.cols, p.t.bn);
+  g.kblocks = (int)p.kblocks;
+  g.kblocks_batch = (int)p.kblocks_batch;
+  g.splits = p.t.splits;
+  g.bias = ep.bias;
+  g.act = ep.act;
+  g.residual = ep.residual.data != nullptr;
+  g.save_z = ep.z.data != nullptr;
+  g.stall = g_stall.load(std::memory_order_relaxed);
+  g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  g.units = p.batches * g.row_tiles * g.col_tiles * g.splits;
+  if (vsa::launch_linear_gemm(g, p.kind, type, sms, st) != cudaSuccess) return VSA_ERR_CUDA;
+  if (!split) return VSA_OK;
+  vsa::FinishParams f{};
+  f.partial = static_cast<const float*>(workspace);
+  f.splits = p.t.splits;
+  f.batches = (int)p.batches;
+  f.rows = (int)p.rows;
+  f.F = (int)p.cols;
+  f.bias = ep.bias;
+  f.act = ep.act;
+  f.residual = ep.residual;
+  f.z = ep.z;
+  f.out = ep.out;
+  return vsa::launch_linear_finish(f, type, sms, st) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+}
+
+vsa_status check_weight(const void* w, long long stride, const vsa_linear_sizes* s) {
+  if (!w) return VSA_ERR_INVALID_ARG;
+  if (!vsa::aligned16(w)) return VSA_ERR_ALIGN;
+  if (s->F > 1 && stride < s->K) return VSA_ERR_INVALID_ARG;
+  if (stride % 8) return VSA_ERR_ALIGN;
+  if (stride >= (1LL << 38)) return VSA_ERR_UNSUPPORTED;
+  return VSA_OK;
+}
+
+vsa_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!need) return VSA_OK;
+  if (!ws) return VSA_ERR_INVALID_ARG;
+  if (!vsa::aligned16(ws)) return VSA_ERR_ALIGN;
+  return have < need ? VSA_ERR_INVALID_ARG : VSA_OK;
+}
+
+size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+
+// Backward workspace: dz, the blocks' column sums, the parts of a split product.
+struct BackwardBytes {
+  size_t dz, sums, parts;
+  size_t total() const { return dz + sums + parts; }
+};
+BackwardBytes backward_bytes(const vsa_linear_sizes* s, int act, bool dx, bool dw, bool db, int sms) {
+  const long long M = (long long)s->B * s->N;
+  BackwardBytes b{};
+  if (act != VSA_ACT_NONE) b.dz = align_up((size_t)M * s->F * 2);
+  if (db) b.sums = align_up((size_t)slope_blocks(M, s->F, sms) * s->F * 4);
+  for (bool join : {false, true}) {
+    if (dx) {
+      Product p = input_product(s, join);
+      p.plan(sms);
+      b.parts = larger(b.parts, p.partial_bytes());
+    }
+    for (bool wide : {false, true})
+      if (dw) {
+        Product p = weight_product(s, join, wide);
+        p.plan(sms);
+        b.parts = larger(b.parts, p.partial_bytes());
+      }
+  }
+  return b;
+}
+
+bool known_activation(int act) { return act >= VSA_ACT_NONE && act <= VSA_ACT_GELU_TANH; }
+
+static_assert(vsa::kActNone == (int)VSA_ACT_NONE && vsa::kActSilu == (int)VSA_ACT_SILU &&
+                  vsa::kActGelu == (int)VSA_ACT_GELU && vsa::kActGeluTanh == (int)VSA_ACT_GELU_TANH,
+              "ABI activations");
+
+}  // namespace
+
+extern "C" {
+
+size_t vsa_linear_workspace_bytes(const vsa_linear_sizes* sizes) {
+  int sms = 0;
+  if (check_sizes(sizes) != VSA_OK || vsa::current_device_sms(&sms) != VSA_OK) return 0;
+  if (!sizes->B || !sizes->N || skinny(sizes)) return 0;
+  size_t n = 0;
+  for (bool join : {false, true}) {
+    Product p = forward_product(sizes, join);
+    p.plan(sms);
+    n = larger(n, p.partial_bytes());
+  }
+  return n;
+}
+
+vsa_status vsa_linear(const vsa_linear_sizes* sizes, const vsa_heads* x, const void* weight, long long weight_stride,
+                      const float* bias, int activation, const vsa_heads* residual, const vsa_heads* z,
+                      const vsa_heads* out, void* workspace, size_t ws_bytes, void* stream) {
+  vsa_status e = check_sizes(sizes);
+  if (e != VSA_OK) return e;
+  if (!known_activation(activation)) return VSA_ERR_UNSUPPORTED;
+  e = check_view(x, sizes, sizes->K, false);
+  if (e == VSA_OK) e = check_view(out, sizes, sizes->F, true);
+  if (e == VSA_OK && residual) e = residual->heads != out->heads ? VSA_ERR_SHAPE : check_view(residual, sizes, sizes->F, false);
+  if (e == VSA_OK && z) e = z->heads != out->heads ? VSA_ERR_SHAPE : check_view(z, sizes, sizes->F, true);
+  if (e == VSA_OK) e = check_weight(weight, weight_stride, sizes);
+  if (e != VSA_OK) return e;
+  if (bias && !vsa::aligned16(bias)) return VSA_ERR_ALIGN;
+  if (!sizes->B || !sizes->N) return VSA_OK;
+  int sms = 0;
+  e = vsa::current_device_sms(&sms);
+  if (e != VSA_OK) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool swap = sizes->N == 1;
+  vsa_linear_sizes rows = *sizes;
+  if (swap) rows.N = sizes->B, rows.B = 1;
+  sizes = &rows;
+  vsa_heads store[4];
+  x = single_token(x, swap, store);
+  residual = single_token(residual, swap, store + 1);
+  z = single_token(z, swap, store + 2);
+  out = single_token(out, swap, store + 3);
+  Epilogue ep{bias, activation, rows_view(residual, sizes->F), rows_view(z, sizes->F), rows_view(out, sizes->F)};
+  const RowsView xv = rows_view(x, sizes->K);
+  if (skinny(sizes)) {
+    vsa::SkinnyParams p{};
+    p.x = xv;
+    p.residual = ep.residual;
+    p.z = ep.z;
+    p.out = ep.out;
+    p.w = weight;
+    p.w_stride = weight_stride;
+    p.bias = bias;
+    p.act = activation;
+    p.rows = sizes->N;
+    p.batches = sizes->B;
+    p.K = sizes->K;
+    p.F = sizes->F;
+    return vsa::launch_linear_skinny(p, sizes->type, st) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+  }
+  Product p = forward_product(sizes, joined(sizes->B, sizes->N, {x, residual, z, out}));
+  p.plan(sms);
+  e = check_workspace(workspace, ws_bytes, p.partial_bytes());
+  if (e != VSA_OK) return e;
+  const RowsView w{const_cast<void*>(weight), 1, sizes->K, 0, 0, weight_stride};
+  return run_product(p, sizes->type, xv, w, sizes->F, ep, workspace, sms, st);
+}
+
+size_t vsa_linear_backward_workspace_bytes(const vsa_linear_sizes* sizes, int activation) {
+  int sms = 0;
+  if (check_sizes(sizes) != VSA_OK || !known_activation(activation) || vsa::current_device_sms(&sms) != VSA_OK) return 0;
+  if (!sizes->B || !sizes->N) return 0;
+  return backward_bytes(sizes, activation, true, true, true, sms).total();
+}
+
+vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x, const void* weight,
+                               long long weight_stride, const vsa_heads* z, int activation, const vsa_heads* dout,
+                               const vsa_heads* dx, void* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  vsa_status e = check_sizes(sizes);
+  if (e != VSA_OK) return e;
+  if (!known_activation(activation)) return VSA_ERR_UNSUPPORTED;
+  e = check_view(dout, sizes, sizes->F, false);
+  if (e == VSA_OK && activation != VSA_ACT_NONE)
+    e = z && z->heads != dout->heads ? VSA_ERR_SHAPE : check_view(z, sizes, sizes->F, false);
+  if (e == VSA_OK && dweight) e = check_view(x, sizes, sizes->K, false);
+  if (e == VSA_OK && dx) e = check_view(dx, sizes, sizes->K, true);
+  if (e == VSA_OK && dx) e = check_weight(weight, weight_stride, sizes);
+  if (e != VSA_OK) return e;
+  if ((dweight && !vsa::aligned16(dweight)) || (dbias && !vsa::aligned16(dbias))) return VSA_ERR_ALIGN;
+  int sms = 0;
+  e = vsa::current_device_sms(&sms);
+  if (e != VSA_OK) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int F = sizes->F, K = sizes->K;
+  if (!sizes->B || !sizes->N) {  // no rows: the sums are 0
+    if (dweight && cudaMemsetAsync(dweight, 0, (size_t)F * K * 2, st) != cudaSuccess) return VSA_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, (size_t)F * 4, st) != cudaSuccess) return VSA_ERR_CUDA;
+    return VSA_OK;
+  }
+  const bool act = activation != VSA_ACT_NONE, swap = sizes->N == 1;
+  vsa_linear_sizes rows = *sizes;
+  if (swap) rows.N = sizes->B, rows.B = 1;
+  sizes = &rows;
+  vsa_heads store[4];
+  x = single_token(x, swap, store);
+  z = single_token(z, swap, store + 1);
+  dout = single_token(dout, swap, store + 2);
+  dx = single_token(dx, swap, store + 3);
+  const BackwardBytes bytes = backward_bytes(sizes, activation, dx != nullptr, dweight != nullptr, dbias != nullptr, sms);
+  e = check_workspace(workspace, ws_bytes, bytes.total());
+  if (e != VSA_OK) return e;
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  RowsView dz = rows_view(dout, F);
+  vsa_heads dz_heads = *dout;
+  if (act || dbias) {
+    vsa::SlopeParams s{};
+    s.dout = dz;
+    if (act) s.z = rows_view(z, F);
+    s.dz = ws;
+    s.partial = dbias ? reinterpret_cast<float*>(ws + bytes.dz) : nullptr;
+    s.act = activation;
+    s.batches = sizes->B;
+    s.rows = sizes->N;
+    s.F = F;
+    s.blocks_y = slope_blocks((long long)sizes->B * sizes->N, F, sms);
+    if (vsa::launch_linear_slope(s, sizes->type, dbias, st) != cudaSuccess) return VSA_ERR_CUDA;
+    if (act) {
+      dz = plain_rows(ws, sizes->N, F);
+      dz_heads = vsa_heads{ws, 1, (long long)sizes->N * F, F, F};
+    }
+  }
+  void* const parts = ws + bytes.dz + bytes.sums;
+  const int M = sizes->B * sizes->N;
+  if (dx) {
+    Product p = input_product(sizes, joined(sizes->B, sizes->N, {&dz_heads, dx}));
+    p.plan(sms);
+    const RowsView w{const_cast<void*>(weight), 1, K, 0, 0, weight_stride};
+    e = run_product(p, sizes->type, dz, w, F, Epilogue{nullptr, 0, {}, {}, rows_view(dx, K)}, parts, sms, st);
+    if (e != VSA_OK) return e;
+  }
+  if (dweight) {
+    const bool join = joined(sizes->B, sizes->N, {&dz_heads, x});
+    Product p = weight_product(sizes, join, x->heads > 1);
+    p.plan(sms);
+    e = run_product(p, sizes->type, dz, rows_view(x, K), join ? M : sizes->N,
+                    Epilogue{nullptr, 0, {}, {}, plain_rows(dweight, F, K)}, parts, sms, st);
+  }
+  return e;
+}
+
+vsa_status vsa_linear_check(void* stream) {
+  int sms = 0, word = 0;
+  vsa_status e = vsa::current_device_sms(&sms);
+  if (e != VSA_OK) return e;
+  if (vsa::linear_error_word(&word, static_cast<cudaStream_t>(stream)) != cudaSuccess) return VSA_ERR_CUDA;
+  return word ? VSA_ERR_TIMEOUT : VSA_OK;
+}
+
+vsa_status vsa_linear_set_limits(uint64_t wait_ns, int stall) {
+  if (!wait_ns) return VSA_ERR_INVALID_ARG;
+  g_wait_ns.store(wait_ns, std::memory_order_relaxed);
+  g_stall.store(stall != 0, std::memory_order_relaxed);
+  return VSA_OK;
+}
+
+}  // extern "C"

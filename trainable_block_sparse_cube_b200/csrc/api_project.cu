@@ -7,25 +7,9 @@
 
 namespace {
 
-static_assert(vsa::kRopePairs == VSA_ROPE_MAX_PAIRS && vsa::kRopeAxes == VSA_ROPE_MAX_AXES, "ABI limits");
+using vsa::check_heads;
 
-// A strided [B, heads, N, D] tensor of `elem`-byte elements.
-vsa_status check_heads(const vsa_heads* x, int B, int N, int elem, bool written) {
-  if (x->heads < 0) return VSA_ERR_SHAPE;
-  if (x->heads > 65535) return VSA_ERR_UNSUPPORTED;
-  if (!B || !N || !x->heads) return VSA_OK;
-  if (!x->data) return VSA_ERR_INVALID_ARG;
-  if (!vsa::aligned16(x->data)) return VSA_ERR_ALIGN;
-  const int len[3] = {B, x->heads, N};
-  const long long stride[3] = {x->s_b, x->s_h, x->s_n};
-  for (int i = 0; i < 3; ++i)
-    if (len[i] > 1) {
-      if (stride[i] < 0 || (written && stride[i] == 0)) return VSA_ERR_INVALID_ARG;
-      if (stride[i] >= (1LL << 40)) return VSA_ERR_UNSUPPORTED;
-      if (stride[i] * elem % 16) return VSA_ERR_ALIGN;
-    }
-  return VSA_OK;
-}
+static_assert(vsa::kRopePairs == VSA_ROPE_MAX_PAIRS && vsa::kRopeAxes == VSA_ROPE_MAX_AXES, "ABI limits");
 
 // The parts of RopeParams that every call shares.
 vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation* r, const vsa_positions* o) {

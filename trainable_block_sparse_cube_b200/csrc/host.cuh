@@ -30,6 +30,24 @@ inline EncodeTiledFn get_encode_fn() {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A strided [B, heads, N, D] tensor of `elem`-byte elements.
+inline vsa_status check_heads(const vsa_heads* x, int B, int N, int elem, bool written) {
+  if (x->heads < 0) return VSA_ERR_SHAPE;
+  if (x->heads > 65535) return VSA_ERR_UNSUPPORTED;
+  if (!B || !N || !x->heads) return VSA_OK;
+  if (!x->data) return VSA_ERR_INVALID_ARG;
+  if (!aligned16(x->data)) return VSA_ERR_ALIGN;
+  const int len[3] = {B, x->heads, N};
+  const long long stride[3] = {x->s_b, x->s_h, x->s_n};
+  for (int i = 0; i < 3; ++i)
+    if (len[i] > 1) {
+      if (stride[i] < 0 || (written && stride[i] == 0)) return VSA_ERR_INVALID_ARG;
+      if (stride[i] >= (1LL << 40)) return VSA_ERR_UNSUPPORTED;
+      if (stride[i] * elem % 16) return VSA_ERR_ALIGN;
+    }
+  return VSA_OK;
+}
+
 // SM count of the current device, or an error if it is not an sm_100 part.
 // The attributes of a device are read once.
 inline vsa_status current_device_sms(int* sms) {

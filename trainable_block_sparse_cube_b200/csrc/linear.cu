@@ -1,0 +1,621 @@
+// Linear product with its epilogue, and its gradients:
+//
+//   forward   y = act(x W^T + b) + res,  z = x W^T + b saved for the backward
+//   backward  dz = dy act'(z);  dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+//
+// x, y, res, z and their gradients are strided views [B, heads, N, D] read and
+// written in place as B x N rows of heads * D channels, so the product takes
+// the attention's output and makes its v without a copy.
+//
+// Three kernels make a product:
+//  * gemm_kernel, tensor cores. A pair of CTAs computes a tile of 256 x bn:
+//    each CTA holds 128 rows of A and half of B's rows, tcgen05.mma
+//    (cta_group::2) reads both halves, so a CTA loads 16 + bn/16 KB a 64-long
+//    step of the contraction instead of the 16 + bn/8 KB of a lone CTA: the
+//    L2 -> SM rate, not the tensor cores, would bound the latter. One thread
+//    issues the loads (5 stages of 32 KB), one the MMAs, eight warps the
+//    epilogue of the tile before (two accumulators of up to 256 columns fill
+//    the SM's tensor memory). Bound by the tensor cores where the product is
+//    large.
+//  * finish_kernel joins the parts of a contraction that was split because it
+//    has too few tiles for 74 pairs, always in the same order.
+//  * skinny_kernel, up to 8 rows: a warp a pair of output columns, bound by
+//    the one pass over W.
+//
+// Sums are fp32; the result is rounded once. dz is rounded to the operands'
+// type before its products, as the tensor cores read it; db is summed from
+// the unrounded values.
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "pair_ptx.cuh"
+#include "vsa_common.cuh"
+
+namespace vsa {
+
+namespace {
+
+using namespace ptx;
+
+__device__ int g_linear_error;
+
+constexpr int kStages = 5, kStageBytes = 32768, kTileA = 16384;
+constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kSlotBytes = 4096;  // 32 rows of 128 bytes
+constexpr int kAccColumns = 256;
+
+struct Barriers {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t residual[kEpiWarps];
+  uint64_t drained;
+  uint32_t tmem;
+};
+constexpr int kGemmSmem = 1024 + kStages * kStageBytes + kEpiWarps * 2 * kSlotBytes + (int)sizeof(Barriers);
+static_assert(kGemmSmem <= 227 * 1024, "shared memory");
+
+// ---------------------------------------------------------------- arithmetic
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<T>(r[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+}
+
+// z s(v) and its slope s + z s (1 - s) v' are silu (v = z) and the tanh form
+// of gelu (v = 2 sqrt(2/pi) (z + 0.044715 z^3)): both keep their relative
+// accuracy where z is far below 0. gelu is z times the normal distribution
+// function, from the complementary error function for the same reason.
+constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.07135481282805f;  // 2 sqrt(2/pi), that times 0.044715
+
+__device__ __forceinline__ float sigmoid_times(float z, float v) { return __fdividef(z, 1.f + __expf(-v)); }
+
+__device__ __forceinline__ float activate(float z, int act) {
+  if (act == kActSilu) return sigmoid_times(z, z);
+  if (act == kActGeluTanh) return sigmoid_times(z, z * fmaf(kTanhB, z * z, kTanhA));
+  if (act == kActGelu) return 0.5f * z * erfcf(-0.7071067811865476f * z);
+  return z;
+}
+
+__device__ __forceinline__ float slope(float z, int act) {
+  if (act == kActSilu) {
+    const float s = __fdividef(1.f, 1.f + __expf(-z));
+    return fmaf(z * s, 1.f - s, s);
+  }
+  if (act == kActGeluTanh) {
+    const float s = __fdividef(1.f, 1.f + __expf(-z * fmaf(kTanhB, z * z, kTanhA)));
+    return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z * z, kTanhA), s);
+  }
+  if (act == kActGelu)  // 1 / sqrt(2 pi)
+    return fmaf(0.3989422804014327f * z, __expf(-0.5f * z * z), 0.5f * erfcf(-0.7071067811865476f * z));
+  return 1.f;
+}
+
+__device__ __forceinline__ void activate8(float (&v)[8], int act) {
+  if (act == kActNone) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate(v[i], act);
+}
+
+__device__ __forceinline__ void add_bias8(float (&v)[8], const float* bias) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(bias)), b = __ldg(reinterpret_cast<const float4*>(bias) + 1);
+  v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+  v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+}
+
+template <typename T>
+__device__ __forceinline__ T* at(const RowsView& v, int b, int n, int c) {
+  return static_cast<T*>(v.data) + b * v.s_b + (c / v.D) * v.s_h + n * v.s_n + c % v.D;
+}
+
+// ---------------------------------------------------------------- tensor cores
+struct Waiter {
+  unsigned long long limit;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    return mbar_wait(bar, parity, limit) || gave_up();
+  }
+  __device__ __forceinline__ bool pair(uint64_t* bar, uint32_t parity) const {  // arrivals of both CTAs
+    return mbar_wait_cluster(bar, parity, limit) || gave_up();
+  }
+  __device__ __forceinline__ static bool gave_up() {
+    atomicOr(&g_linear_error, kErrTimeout);
+    return false;
+  }
+};
+
+// A work unit: one tile of one part of the contraction, neighbours in columns
+// first (the pairs that run together then share their rows of A in L2).
+struct Unit {
+  int batch, row0, col0, split, k0, k1;
+  __device__ __forceinline__ Unit(const GemmParams& p, long long u) {
+    const long long tiles = (long long)p.batches * p.row_tiles * p.col_tiles;
+    split = (int)(u / tiles);
+    const long long t = u - split * tiles;
+    const int rt = (int)(t / p.col_tiles);
+    col0 = (int)(t - (long long)rt * p.col_tiles) * p.bn;
+    batch = rt / p.row_tiles;
+    row0 = (rt - batch * p.row_tiles) * 256;
+    k0 = (int)((long long)p.kblocks * split / p.splits);
+    k1 = (int)((long long)p.kblocks * (split + 1) / p.splits);
+  }
+};
+
+// KIND kGemmForward: A and B K-major. kGemmInput: A K-major, B MN-major.
+// kGemmWeight: both MN-major, the contraction running over batches of rows.
+template <int KIND, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* const slots = raw + (base - smem_u32(raw)) + kStages * kStageBytes;
+  Barriers& sh = *reinterpret_cast<Barriers*>(slots + kEpiWarps * 2 * kSlotBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int half = p.bn / 2;  // rows of B in a CTA
+  const Waiter wait{p.wait_ns};
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(&sh.residual[i], 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init();
+    prefetch_tmap(&p.ta);
+    prefetch_tmap(&p.tb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&sh.tmem, 512);
+    tmem_relinquish_pair();
+  }
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- loads of this CTA's operand rows; both CTAs' complete on the even CTA's barriers
+      const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : (half + 63) / 64 * 8192;
+      const uint32_t pair_bytes = 2 * (kTileA + b_bytes);
+      int it = 0;
+      bool ok = true;
+      for (long long u = pair; ok && u < p.units; u += pairs) {
+        const Unit w(p, u);
+        const int row = w.row0 + (int)rank * 128, col = w.col0 + (int)rank * half;
+        for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+          const int s = it % kStages, use = it / kStages;
+          if (use && !wait(&sh.empty[s], (use - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], pair_bytes);
+          if (p.stall) continue;
+          const uint32_t bar = mapa(smem_u32(&sh.full[s]), 0);
+          const uint32_t a = base + s * kStageBytes, b = a + kTileA;
+          if (KIND == kGemmWeight) {
+            const int kbatch = kb / p.kblocks_batch, k = (kb - kbatch * p.kblocks_batch) * 64;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int c = row + 64 * j, h = c / p.a_d;
+              tma_load_4d<2>(a + j * 8192, &p.ta, bar, c - h * p.a_d, k, h, kbatch);
+            }
+            for (int j = 0; j * 64 < half; ++j) {
+              const int c = col + 64 * j, h = c / p.b_d;
+              tma_load_4d<2>(b + j * 8192, &p.tb, bar, c - h * p.b_d, k, h, kbatch);
+            }
+          } else {
+            const int k = kb * 64, h = k / p.a_d;
+            tma_load_4d<2>(a, &p.ta, bar, k - h * p.a_d, row, h, w.batch);
+            if (KIND == kGemmForward) {
+              tma_load_4d<2>(b, &p.tb, bar, k, col, 0, 0);
+            } else {
+              for (int j = 0; j * 64 < half; ++j) tma_load_4d<2>(b + j * 8192, &p.tb, bar, col + 64 * j, k, 0, 0);
+            }
+          }
+        }
+      }
+      if (!ok && rank == 0)  // the loads in flight land before the pair's shared memory goes
+        for (int i = it > kStages ? it - kStages : 0; i < it; ++i) mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, p.wait_ns);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // ---- MMAs of the pair
+      const uint32_t idesc = idesc_f16_f32(256, p.bn, KIND == kGemmWeight, KIND != kGemmForward, std::is_same<T, __nv_bfloat16>::value);
+      constexpr uint32_t A_STEP = (KIND == kGemmWeight ? 2048 : 32) >> 4, B_STEP = (KIND == kGemmForward ? 32 : 2048) >> 4;
+      int it = 0, tile = 0;
+      bool ok = true;
+      for (long long u = pair; ok && u < p.units; u += pairs, ++tile) {
+        const Unit w(p, u);
+        const int buf = tile & 1, use = tile >> 1;
+        if (use && !wait.pair(&sh.acc_empty[buf], (use - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!wait(&sh.full[s], (it / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = base + s * kStageBytes;
+          const uint64_t ad = sdesc_sw128(a, KIND == kGemmWeight ? 8192 : 16, 1024);
+          const uint64_t bd = sdesc_sw128(a + kTileA, KIND == kGemmForward ? 16 : 8192, 1024);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_f16_ss_pair(tmem + buf * kAccColumns, ad + i * A_STEP, bd + i * B_STEP, idesc, kb > w.k0 || i);
+          mma_commit_pair(&sh.empty[s]);
+        }
+        if (ok) mma_commit_pair(&sh.acc_full[buf]);
+      }
+      if (!ok) {  // the MMAs in flight end before the tensor memory goes
+        mma_commit_pair(&sh.drained);
+        mbar_wait(&sh.drained, 0, p.wait_ns);
+      }
+    }
+  } else {
+    // ---- epilogue: a warp takes 32 rows and every second 64-column group of the tile
+    const int ew = warp - 2, quarter = warp & 3;
+    uint8_t* const slot0 = slots + ew * 2 * kSlotBytes;
+    const uint32_t slot0_addr = smem_u32(slot0);
+    const int sw = lane & 7;
+    const uint32_t lane_off = lane * 128;
+    int tile = 0, flip = 0;
+    uint32_t res_phase = 0;
+    bool ok = true;
+    for (long long u = pair; ok && u < p.units; u += pairs, ++tile) {
+      const Unit w(p, u);
+      const int buf = tile & 1;
+      if (!__all_sync(0xffffffffu, wait(&sh.acc_full[buf], (tile >> 1) & 1))) break;
+      tc_fence_after();
+      const int row = w.row0 + (int)rank * 128 + quarter * 32;
+      for (int g = ew >> 2; g * 64 < p.bn; g += 2) {
+        const int col = w.col0 + g * 64;
+        if (row >= p.rows || col >= p.F) break;
+        const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 64);
+        if (p.splits > 1) {
+          // a part of the contraction: fp32 sums, 32 columns a store
+#pragma unroll 1
+          for (int h = 0; h < 2 && col + 32 * h < p.F; ++h, flip ^= 1) {
+            uint32_t r[32];
+            tmem_ld32(acc + 32 * h, r);
+            if (lane == 0) bulk_wait_read<1>();
+            tmem_wait_ld();
+            __syncwarp();
+            uint8_t* const mine = slot0 + flip * kSlotBytes + lane_off;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(mine + ((j ^ sw) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_4d(&p.tout, slot0_addr + flip * kSlotBytes, col + 32 * h, row, w.batch, w.split);
+              bulk_commit();
+            }
+          }
+          continue;
+        }
+        const int head = col / p.o_d, c = col - head * p.o_d;
+        const bool save_z = p.save_z != 0;
+        if (lane == 0) {
+          if (save_z) bulk_wait_read<0>();
+          else bulk_wait_read<1>();
+          if (p.residual) {
+            mbar_arrive_expect_tx(&sh.residual[ew], kSlotBytes);
+            tma_load_4d<1>(slot0_addr + flip * kSlotBytes, &p.tres, smem_u32(&sh.residual[ew]), c, row, head, w.batch);
+          }
+        }
+        __syncwarp();
+        uint8_t* const mine = slot0 + flip * kSlotBytes + lane_off;
+        uint8_t* const mine_z = slot0 + (flip ^ 1) * kSlotBytes + lane_off;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tmem_ld32(acc + 32 * h, r);
+          tmem_wait_ld();
+          if (h == 0 && p.residual) {
+            if (!__all_sync(0xffffffffu, wait(&sh.residual[ew], res_phase))) ok = false;
+            res_phase ^= 1;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
+            const int cj = col + 32 * h + 8 * j;
+            if (p.bias && cj < p.F) add_bias8(v, p.bias + cj);
+            const int off = ((4 * h + j) ^ sw) << 4;
+            if (save_z) *reinterpret_cast<uint4*>(mine_z + off) = pack8<T>(v);
+            activate8(v, p.act);
+            if (p.residual) {
+              float x[8];
+              unpack8<T>(*reinterpret_cast<const uint4*>(mine + off), x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] += x[i];
+            }
+            *reinterpret_cast<uint4*>(mine + off) = pack8<T>(v);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_4d(&p.tout, slot0_addr + flip * kSlotBytes, c, row, head, w.batch);
+          if (save_z) tma_store_4d(&p.tz, slot0_addr + (flip ^ 1) * kSlotBytes, c, row, head, w.batch);
+          bulk_commit();
+        }
+        flip ^= 1;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sh.acc_empty[buf]), 0));
+    }
+    if (lane == 0) bulk_wait0();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------- split contractions
+// out = act(sum of the parts + bias) + residual, 8 columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
+  const int groups = p.F / 8;
+  const long long n8 = (long long)p.batches * p.rows * groups, part = (long long)p.batches * p.rows * p.F;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += (long long)gridDim.x * blockDim.x) {
+    const long long m = i / groups;
+    const int c = (int)(i - m * groups) * 8;
+    const int b = (int)(m / p.rows), n = (int)(m - (long long)b * p.rows);
+    const float* src = p.partial + m * p.F + c;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(src + s * part));
+      const float4 y = __ldcs(reinterpret_cast<const float4*>(src + s * part) + 1);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+    if (p.bias) add_bias8(v, p.bias + c);
+    if (p.z.data) *reinterpret_cast<uint4*>(at<T>(p.z, b, n, c)) = pack8<T>(v);
+    activate8(v, p.act);
+    if (p.residual.data) {
+      float x[8];
+      unpack8<T>(*reinterpret_cast<const uint4*>(at<T>(p.residual, b, n, c)), x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += x[k];
+    }
+    *reinterpret_cast<uint4*>(at<T>(p.out, b, n, c)) = pack8<T>(v);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+constexpr int kSkinnyK = 2048;  // channels of x staged at a time
+
+// R >= batches * rows rows; a warp computes two columns of all of them, its
+// lanes 8 channels apart along W's row.
+template <int R, typename T>
+__global__ void __launch_bounds__(256) skinny_kernel(const SkinnyParams p) {
+  __shared__ uint4 xs[R][kSkinnyK / 8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int M = p.batches * p.rows;
+  const int f0 = (blockIdx.x * 8 + warp) * 2;
+  float acc[2][R];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[f][r] = 0.f;
+  const T* const w = static_cast<const T*>(p.w);
+  for (int k0 = 0; k0 < p.K; k0 += kSkinnyK) {
+    const int len = min(kSkinnyK, p.K - k0) / 8;
+    if (k0) __syncthreads();
+    for (int i = threadIdx.x; i < R * len; i += 256) {
+      const int r = i / len, c = i - r * len;
+      xs[r][c] = r < M ? *reinterpret_cast<const uint4*>(at<T>(p.x, r / p.rows, r % p.rows, k0 + c * 8)) : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (f0 < p.F) {  // F is a multiple of 8: both columns lie inside
+#pragma unroll 4
+      for (int c = lane; c < len; c += 32) {
+        float a[2][8];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+          unpack8<T>(__ldg(reinterpret_cast<const uint4*>(w + (f0 + f) * p.w_stride + k0) + c), a[f]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float x[8];
+          unpack8<T>(xs[r][c], x);
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[f][r] = fmaf(a[f][i], x[i], acc[f][r]);
+        }
+      }
+    }
+  }
+  if (f0 >= p.F) return;
+  float mine = 0.f;
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) acc[f][r] += __shfl_xor_sync(0xffffffffu, acc[f][r], o);
+      if (lane == f * R + r) mine = acc[f][r];
+    }
+  const int f = lane / R, r = lane % R;
+  if (f < 2 && r < M) {
+    const int c = f0 + f, b = r / p.rows, n = r % p.rows;
+    if (p.bias) mine += p.bias[c];
+    if (p.z.data) *at<T>(p.z, b, n, c) = static_cast<T>(mine);
+    mine = activate(mine, p.act);
+    if (p.residual.data) mine += static_cast<float>(*at<T>(p.residual, b, n, c));
+    *at<T>(p.out, b, n, c) = static_cast<T>(mine);
+  }
+}
+
+// ---------------------------------------------------------------- dz and db
+// A block takes 256 columns and every blocks_y-th group of 8 rows; a thread 8
+// columns, whose sum it keeps.
+template <typename T>
+__global__ void __launch_bounds__(256) slope_kernel(const SlopeParams p) {
+  __shared__ float part[8][32][9];
+  const int tx = threadIdx.x, ty = threadIdx.y;
+  const int c = (blockIdx.x * 32 + tx) * 8;
+  const unsigned M = (unsigned)p.batches * p.rows;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < p.F) {
+    const T* const dsrc = at<T>(p.dout, 0, 0, c);
+    const T* const zsrc = p.act != kActNone ? at<T>(p.z, 0, 0, c) : nullptr;
+    T* const dst = static_cast<T*>(p.dz) + c;
+#pragma unroll 2
+    for (unsigned m = blockIdx.y * 8 + ty; m < M; m += gridDim.y * 8) {
+      const unsigned b = m / (unsigned)p.rows, n = m - b * (unsigned)p.rows;
+      float v[8];
+      unpack8<T>(*reinterpret_cast<const uint4*>(dsrc + b * p.dout.s_b + n * p.dout.s_n), v);
+      if (p.act != kActNone) {
+        float z[8];
+        unpack8<T>(*reinterpret_cast<const uint4*>(zsrc + b * p.z.s_b + n * p.z.s_n), z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= slope(z[i], p.act);
+        *reinterpret_cast<uint4*>(dst + (long long)m * p.F) = pack8<T>(v);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+  }
+  if (!p.partial) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[ty][tx][i] = sum[i];
+  __syncthreads();
+  const int t = ty * 32 + tx, o = blockIdx.x * 256 + t;
+  if (o < p.F) {
+    float s = 0.f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) s += part[y][t / 8][t % 8];
+    p.partial[(long long)blockIdx.y * p.F + o] = s;
+  }
+}
+
+// db = sum of the blocks' column sums, 32 columns a block, always in the same order.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* partial, int blocks, int F, float* db) {
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float a = 0.f;
+  if (c < F)
+    for (int b = threadIdx.y; b < blocks; b += 32) a += partial[(long long)b * F + c];
+  s[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  float v = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int oc = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && oc < F) db[oc] = v;
+}
+
+template <int KIND, typename T>
+cudaError_t launch_gemm(const GemmParams& p, int num_sms, cudaStream_t st) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> ready[kMaxDevices];  // the attribute belongs to the device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(gemm_kernel<KIND, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+  }
+  const long long pairs = p.units < num_sms / 2 ? p.units : num_sms / 2;
+  gemm_kernel<KIND, T><<<(unsigned)(2 * pairs), kThreads, kGemmSmem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_gemm_kind(const GemmParams& p, int kind, int num_sms, cudaStream_t st) {
+  if (kind == kGemmForward) return launch_gemm<kGemmForward, T>(p, num_sms, st);
+  if (kind == kGemmInput) return launch_gemm<kGemmInput, T>(p, num_sms, st);
+  return launch_gemm<kGemmWeight, T>(p, num_sms, st);
+}
+
+template <typename T>
+cudaError_t launch_skinny(const SkinnyParams& p, cudaStream_t st) {
+  const int M = p.batches * p.rows, blocks = (p.F + 15) / 16;
+  if (M <= 1) skinny_kernel<1, T><<<blocks, 256, 0, st>>>(p);
+  else if (M <= 2) skinny_kernel<2, T><<<blocks, 256, 0, st>>>(p);
+  else if (M <= 4) skinny_kernel<4, T><<<blocks, 256, 0, st>>>(p);
+  else skinny_kernel<8, T><<<blocks, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_sms, cudaStream_t st) {
+  return type ? launch_gemm_kind<__half>(p, kind, num_sms, st) : launch_gemm_kind<__nv_bfloat16>(p, kind, num_sms, st);
+}
+
+cudaError_t launch_linear_finish(const FinishParams& p, int type, int num_sms, cudaStream_t st) {
+  const long long blocks = ((long long)p.batches * p.rows * (p.F / 8) + 255) / 256, most = 8LL * num_sms;
+  const int grid = (int)(blocks < most ? blocks : most);
+  if (type) finish_kernel<__half><<<grid, 256, 0, st>>>(p);
+  else finish_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_skinny(const SkinnyParams& p, int type, cudaStream_t st) {
+  return type ? launch_skinny<__half>(p, st) : launch_skinny<__nv_bfloat16>(p, st);
+}
+
+cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaStream_t st) {
+  const dim3 grid((p.F + 255) / 256, p.blocks_y), block(32, 8);
+  if (type) slope_kernel<__half><<<grid, block, 0, st>>>(p);
+  else slope_kernel<__nv_bfloat16><<<grid, block, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.partial) return e;
+  column_sum_kernel<<<(p.F + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, p.blocks_y, p.F, db);
+  return cudaGetLastError();
+}
+
+cudaError_t linear_error_word(int* word, cudaStream_t st) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  static const int zero = 0;
+  if (e == cudaSuccess && *word) e = cudaMemcpyToSymbolAsync(g_linear_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+  return e;
+}
+
+}  // namespace vsa

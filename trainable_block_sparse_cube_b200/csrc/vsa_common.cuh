@@ -189,6 +189,73 @@ cudaError_t launch_rope(RopeParams p, int type, int num_sms, cudaStream_t st);
 size_t norm_rope_partial_bytes(int D, int num_sms);
 cudaError_t launch_norm_rope_backward(RopeParams p, int type, float* dwq, float* dwk, int num_sms, cudaStream_t st);
 
+// ---------------------------------------------------------------- linear product
+enum : int { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3 };
+
+// A strided 16-bit tensor [B, heads, N, D] seen as B x N rows of heads * D channels.
+struct RowsView {
+  void* data;
+  int heads, D;
+  long long s_b, s_h, s_n;
+};
+
+// out = A B^T on the tensor cores. A, out, the residual and z are 4-D maps
+// (channel of a head, row, head, batch), B of the weights (column, row, 1, 1),
+// in 128-byte swizzle with boxes of 64 channels. A K-major operand is read along
+// its channels, an MN-major one along its rows.
+struct GemmParams {
+  CUtensorMap ta, tb, tout, tres, tz;
+  int a_d, b_d, o_d;        // channels of a head of A, B, out
+  int bn;                   // columns of a tile: 128, 192 or 256
+  int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
+  int rows;                 // rows of a batch
+  int F, col_tiles;         // columns
+  int kblocks;              // 64-long blocks of the contraction
+  int kblocks_batch;        // kGemmWeight: blocks of a batch of rows
+  int splits;               // > 1: tout is fp32 [splits, batches, rows, F] (32-column boxes), see FinishParams
+  const float* bias;        // [F] or null
+  int act, residual, save_z;
+  int stall;                // test hook: no operand is loaded
+  unsigned long long wait_ns;
+  long long units;          // tiles x splits
+};
+
+// Sums the parts of a split contraction and applies the epilogue.
+struct FinishParams {
+  const float* partial;
+  int splits, batches, rows, F;
+  const float* bias;
+  int act;
+  RowsView residual, z, out;   // data null: none
+};
+
+struct SkinnyParams {
+  RowsView x, residual, z, out;
+  const void* w;
+  long long w_stride;
+  const float* bias;
+  int act, rows, batches, K, F;
+};
+
+// dz = dout act'(z) (with an activation) and column sums of dz in fp32.
+struct SlopeParams {
+  RowsView dout, z;
+  void* dz;                 // [batches * rows, F], with an activation
+  float* partial;           // [blocks_y, F] column sums or null
+  int act, batches, rows, F;
+  int blocks_y;
+};
+
+enum : int { kGemmForward = 0, kGemmInput = 1, kGemmWeight = 2 };
+constexpr int kSkinnyRows = 8;
+// type: 0 bf16, 1 fp16
+cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_finish(const FinishParams& p, int type, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_skinny(const SkinnyParams& p, int type, cudaStream_t st);
+cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaStream_t st);
+// Reads and clears the current device's error word of the linear kernels (synchronises the stream).
+cudaError_t linear_error_word(int* word, cudaStream_t st);
+
 cudaError_t launch_gather(const GatherParams& p, int D, int num_sms, cudaStream_t st);
 cudaError_t launch_coarse(const CoarseParams& p, cudaStream_t st);
 cudaError_t launch_fine(const FineParams& p, int D, int grid, cudaStream_t st);

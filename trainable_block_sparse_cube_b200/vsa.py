@@ -25,10 +25,12 @@ EXPORTED = ["vsa_workspace_bytes", "vsa_workspace_layout", "vsa_plan", "vsa_run"
             "vsa_run_train", "vsa_backward_workspace_bytes", "vsa_run_backward", "vsa_backward_stage_times",
             "vsa_stage_times_history", "vsa_backward_stage_times_history",
             "vsa_rope", "vsa_rope_backward", "vsa_qk_norm_rope", "vsa_qk_norm_rope_backward_workspace_bytes",
-            "vsa_qk_norm_rope_backward"]
+            "vsa_qk_norm_rope_backward", "vsa_linear_workspace_bytes", "vsa_linear",
+            "vsa_linear_backward_workspace_bytes", "vsa_linear_backward", "vsa_linear_check", "vsa_linear_set_limits"]
 
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ROPE_MAX_PAIRS, ROPE_MAX_AXES = 128, 4
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 
 class VSAError(RuntimeError):
@@ -66,6 +68,11 @@ class Positions(ctypes.Structure):
 
 class RopeSizes(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("B", ctypes.c_int), ("N", ctypes.c_int), ("D", ctypes.c_int)]
+
+
+class LinearSizes(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("B", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("F", ctypes.c_int)]
 
 
 _lib = None
@@ -140,6 +147,18 @@ def load():
     L.vsa_qk_norm_rope_backward_workspace_bytes.restype = sz
     L.vsa_qk_norm_rope_backward.argtypes = what + [H, H, vp, vp, ctypes.c_float, H, H, H, H, vp, vp, vp, sz, vp]
     L.vsa_qk_norm_rope_backward.restype = i32
+    L.vsa_linear_workspace_bytes.argtypes = [F(LinearSizes)]
+    L.vsa_linear_workspace_bytes.restype = sz
+    L.vsa_linear.argtypes = [F(LinearSizes), H, vp, ctypes.c_longlong, vp, i32, H, H, H, vp, sz, vp]
+    L.vsa_linear.restype = i32
+    L.vsa_linear_backward_workspace_bytes.argtypes = [F(LinearSizes), i32]
+    L.vsa_linear_backward_workspace_bytes.restype = sz
+    L.vsa_linear_backward.argtypes = [F(LinearSizes), H, vp, ctypes.c_longlong, H, i32, H, H, vp, vp, vp, sz, vp]
+    L.vsa_linear_backward.restype = i32
+    L.vsa_linear_check.argtypes = [vp]
+    L.vsa_linear_check.restype = i32
+    L.vsa_linear_set_limits.argtypes = [ctypes.c_uint64, i32]
+    L.vsa_linear_set_limits.restype = i32
     _lib = L
     return L
 
@@ -592,3 +611,115 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, rotation, gr
                                            _ptr(dwq), _ptr(dwk), _ptr(ws), nb, _stream()),
                "vsa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
+
+
+def _need_rows(t, name, dtype=None, device=None, shape=None):
+    """A 16-bit CUDA tensor [B, N, channels] or [B, heads, N, D] whose channels are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must have shape [B, N, channels] or [B, heads, N, D], got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+
+
+def _rows(t):
+    if t is None:
+        return None
+    s = t.stride()
+    if len(s) == 3:
+        return Heads(t.data_ptr(), 1, s[0], 0, s[1])
+    return Heads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
+
+
+def _linear_sizes(x, weight, activation):
+    _need_rows(x, "x")
+    shape = x.shape
+    B, N, K = shape if len(shape) == 3 else (shape[0], shape[2], shape[1] * shape[3])
+    if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.device != x.device:
+        raise ValueError(f"weight must be a CUDA tensor on {x.device}")
+    if weight.dtype != x.dtype:
+        raise ValueError(f"weight must be {x.dtype}, got {weight.dtype}")
+    if weight.dim() != 2 or weight.shape[1] != K:
+        raise ValueError(f"weight must have shape [F, {K}], got {tuple(weight.shape)}")
+    if weight.stride(1) != 1:
+        raise ValueError("weight must have contiguous rows")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    return LinearSizes(TYPES[x.dtype], B, N, K, weight.shape[0])
+
+
+def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out=None, z=None):
+    """act(x weight^T + bias) + residual. x is [B, N, K], or [B, heads, N, D] in the attention's layout (rows of
+    K = heads * D channels, D a multiple of 64 if heads > 1), of any strides with contiguous channels; weight
+    [F, K]; bias [F] fp32; activation None, "silu", "gelu" or "gelu_tanh". Returns [B, N, F], or
+    [B, heads, N, F / heads] if ``heads`` is given; ``residual``, ``out`` and ``z`` (which receives
+    x weight^T + bias for linear_backward) have that shape. out may be the residual. Enqueued on the current
+    stream."""
+    sizes = _linear_sizes(x, weight, activation)
+    device, F = x.device, sizes.F
+    if bias is not None:
+        _need_weight(bias, "bias", F, device)
+    if heads is None:
+        shape = torch.Size((sizes.B, sizes.N, F))
+    elif heads < 1 or F % heads:
+        raise ValueError(f"{F} channels do not split into {heads} heads")
+    else:
+        shape = torch.Size((sizes.B, heads, sizes.N, F // heads))
+    for t, name in ((residual, "residual"), (out, "out"), (z, "z")):
+        if t is not None:
+            _need_rows(t, name, x.dtype, device, shape)
+    with _OnDevice(device):
+        L = load()
+        if out is None:
+            out = torch.empty(shape, dtype=x.dtype, device=device)
+        nb = L.vsa_linear_workspace_bytes(sizes)
+        ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+        _check(L.vsa_linear(sizes, _rows(x), weight.data_ptr(), weight.stride(0), _ptr(bias), ACTIVATIONS[activation],
+                            _rows(residual), _rows(z), _rows(out), _ptr(ws), nb, _stream()), "vsa_linear")
+    return out
+
+
+def linear_backward(x, weight, dout, z=None, activation=None, bias=False, dx=None, want=(True, True)):
+    """Gradients of linear from that of its output (whose shape dout has): (dx, dweight, dbias). z is what linear
+    stored, needed with an activation; dbias (fp32) is None unless ``bias``; ``want`` switches dx and dweight
+    off. dx is in the order of dimensions that x is stored in unless given. The residual's gradient is dout.
+    Enqueued on the current stream."""
+    sizes = _linear_sizes(x, weight, activation)
+    device, F = x.device, sizes.F
+    _need_rows(dout, "dout", x.dtype, device)
+    s = dout.shape
+    if (s if len(s) == 3 else (s[0], s[2], s[1] * s[3])) != (sizes.B, sizes.N, F):
+        raise ValueError(f"dout must have shape [{sizes.B}, {sizes.N}, {F}] or [{sizes.B}, heads, {sizes.N}, D], "
+                         f"got {tuple(s)}")
+    if activation is not None:
+        _need_rows(z, "z", x.dtype, device, s)
+    if dx is not None:
+        _need_rows(dx, "dx", x.dtype, device, x.shape)
+    with _OnDevice(device):
+        L = load()
+        if want[0] and dx is None:
+            dx = torch.empty_like(x)
+        dw = torch.empty(weight.shape, dtype=x.dtype, device=device) if want[1] else None
+        db = torch.empty(F, dtype=torch.float32, device=device) if bias else None
+        nb = L.vsa_linear_backward_workspace_bytes(sizes, ACTIVATIONS[activation])
+        ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+        _check(L.vsa_linear_backward(sizes, _rows(x), weight.data_ptr(), weight.stride(0),
+                                     _rows(z) if activation is not None else None, ACTIVATIONS[activation],
+                                     _rows(dout), _rows(dx) if want[0] else None, _ptr(dw), _ptr(db), _ptr(ws), nb,
+                                     _stream()), "vsa_linear_backward")
+    return (dx if want[0] else None), dw, db
+
+
+def linear_check(device=None):
+    """Synchronises the current stream of the device and raises VSAError if a wait inside a linear product on it
+    gave up since the last check."""
+    device = torch.device("cuda" if device is None else device)
+    with _OnDevice(torch.device("cuda", torch.cuda.current_device()) if device.index is None else device):
+        _check(load().vsa_linear_check(_stream()), "vsa_linear_check")
