@@ -15,31 +15,37 @@ std::atomic<int> g_stall{0};
 inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// How a product of `batches` x `rows` x `cols` over `kblocks` 64-long steps is cut.
+// How a product of `batches` x `rows` x `cols` over `kblocks` 64-long steps is
+// cut: `whole` tiles of 256 x bn, and `rest` tiles in `splits` parts each.
 struct Tiling {
   int bn, splits;
+  long long whole, rest;
 };
 
-// The pairs run in rounds; a round costs its steps (the MMA of a step takes
-// 2 bn cycles, its loads 16 + bn/16 KB at the 47 bytes a cycle that an SM gets
-// of the L2's rate) plus the start and the epilogue of a tile, and a split
-// contraction a second kernel that reads the parts again. bn = 192 fills the
-// last round where 256 leaves it short; `wide` excludes it where a tile's
-// second half would start inside a head.
+// The pairs of CTAs run in rounds; a round costs its steps (the MMA of a step
+// takes 2 bn cycles, its loads 16 + bn/16 KB at the 47 bytes a cycle that an
+// SM gets of the L2's rate) plus the start of a tile, and at the end there is
+// an epilogue. The last round's tiles are too few for all pairs and are split
+// along the contraction, which costs a second kernel that reads the parts.
+// `wide` excludes bn = 192 where a tile's second half would start inside a
+// head.
 Tiling choose(long long batches, long long rows, long long cols, long long kblocks, int sms, bool wide) {
   const long long pairs = sms / 2;
-  Tiling best{256, 1};
+  Tiling best{};
   double best_cost = -1;
   for (int bn : {256, 192, 128}) {
     if (wide && bn == 192) continue;
-    const long long tiles = batches * ceil_div(rows, 256) * ceil_div(cols, bn);
+    const long long tiles = batches * ceil_div(rows, 256) * ceil_div(cols, bn), whole = tiles / pairs * pairs;
+    const long long rest = tiles - whole;
     const double load = (16384 + 64.0 * bn) / 47, step = load > 2.0 * bn ? load : 2.0 * bn;
-    for (int s = 1; s <= 32 && s <= kblocks; ++s) {
-      if (s > 1 && tiles * (s - 1) >= pairs) break;  // every pair has work already
-      const long long rounds = ceil_div(tiles * s, pairs);
-      double cost = rounds * (ceil_div(kblocks, s) * step + 800) + 12.0 * bn;
-      if (s > 1) cost += 5000 + 8.0 * s * batches * rows * cols / 2700;
-      if (best_cost < 0 || cost < best_cost) best_cost = cost, best = Tiling{bn, s};
+    const double base = whole / pairs * (kblocks * step + 800) + 12.0 * bn;
+    for (int s = 1; s <= 32 && s <= kblocks && (s == 1 || rest * (s - 1) < pairs); ++s) {
+      double cost = base + ceil_div(rest * s, pairs) * (ceil_div(kblocks, s) * step + 800);
+      if (s > 1) cost += 5000 + 8.0 * s * rest * 256 * bn / 2700;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best = s > 1 ? Tiling{bn, s, whole, rest} : Tiling{bn, 1, tiles, 0};
+      }
     }
   }
   return best;
@@ -53,7 +59,7 @@ struct Product {
   Tiling t;
 
   void plan(int sms) { t = choose(batches, rows, cols, kblocks, sms, wide); }
-  size_t partial_bytes() const { return t.splits > 1 ? align_up((size_t)t.splits * batches * rows * cols * 4) : 0; }
+  size_t partial_bytes() const { return (size_t)t.rest * t.splits * 256 * t.bn * 4; }
 };
 
 // The batches of a call are one run of rows if every view allows it.
@@ -137,22 +143,31 @@ RowsView plain_rows(void* data, long long N, int channels) {
 }
 
 // 4-D map (channel of a head, row, head, batch), 128-byte swizzle.
-vsa_status encode(CUtensorMap* m, const RowsView& v, long long rows, long long batches, int box_rows, int type,
-                  bool fp32 = false) {
+vsa_status encode(CUtensorMap* m, const RowsView& v, long long rows, long long batches, int box_rows, int type) {
   vsa::EncodeTiledFn enc = vsa::get_encode_fn();
   if (!enc) return VSA_ERR_CUDA;
-  const int elem = fp32 ? 4 : 2;
   const cuuint64_t dims[4] = {(cuuint64_t)v.D, (cuuint64_t)rows, (cuuint64_t)v.heads, (cuuint64_t)batches};
   // strides of dimensions of length 1 are not used, but have to be valid
-  const cuuint64_t row = (cuuint64_t)v.D * elem;
-  const cuuint64_t strides[3] = {rows > 1 ? (cuuint64_t)v.s_n * elem : row, v.heads > 1 ? (cuuint64_t)v.s_h * elem : row,
-                                 batches > 1 ? (cuuint64_t)v.s_b * elem : row};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
-  const CUtensorMapDataType dt = fp32      ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                 : type    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return enc(m, dt, 4, v.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+  const cuuint64_t row = (cuuint64_t)v.D * 2;
+  const cuuint64_t strides[3] = {rows > 1 ? (cuuint64_t)v.s_n * 2 : row, v.heads > 1 ? (cuuint64_t)v.s_h * 2 : row,
+                                 batches > 1 ? (cuuint64_t)v.s_b * 2 : row};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  return enc(m, type ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.data, dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? VSA_OK
+             : VSA_ERR_CUDA;
+}
+
+// The parts of split tiles: `rows` rows of bn fp32, written in boxes of 32 x 32.
+vsa_status encode_parts(CUtensorMap* m, void* data, long long rows, int bn) {
+  vsa::EncodeTiledFn enc = vsa::get_encode_fn();
+  if (!enc) return VSA_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)bn, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bn * 4};
+  const cuuint32_t box[2] = {32, 32}, one[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                 CUDA_SUCCESS
              ? VSA_OK
              : VSA_ERR_CUDA;
 }
@@ -173,18 +188,10 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   const int half = p.t.bn / 2;
   vsa_status e = encode(&g.ta, a, run_rows, runs, weight ? 64 : 128, type);
   if (e == VSA_OK) e = encode(&g.tb, b, b_rows, weight ? runs : 1, p.kind == vsa::kGemmForward ? half : 64, type);
-  const bool split = p.t.splits > 1;
-  if (e == VSA_OK) {
-    if (split) {
-      RowsView parts{workspace, (int)p.batches, (int)p.cols, (long long)p.batches * p.rows * p.cols,
-                     (long long)p.rows * p.cols, p.cols};
-      e = encode(&g.tout, parts, p.rows, p.t.splits, 32, type, true);
-    } else {
-      e = encode(&g.tout, ep.out, p.rows, p.batches, 32, type);
-      if (e == VSA_OK && ep.residual.data) e = encode(&g.tres, ep.residual, p.rows, p.batches, 32, type);
-      if (e == VSA_OK && ep.z.data) e = encode(&g.tz, ep.z, p.rows, p.batches, 32, type);
-    }
-  }
+  if (e == VSA_OK) e = encode(&g.tout, ep.out, p.rows, p.batches, 32, type);
+  if (e == VSA_OK && ep.residual.data) e = encode(&g.tres, ep.residual, p.rows, p.batches, 32, type);
+  if (e == VSA_OK && ep.z.data) e = encode(&g.tz, ep.z, p.rows, p.batches, 32, type);
+  if (e == VSA_OK && p.t.rest) e = encode_parts(&g.tpart, workspace, p.t.rest * p.t.splits * 256, p.t.bn);
   if (e != VSA_OK) return e;
   g.a_d = a.D;
   g.b_d = b.D;
@@ -197,28 +204,37 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   g.col_tiles = (int)ceil_div(p.cols, p.t.bn);
   g.kblocks = (int)p.kblocks;
   g.kblocks_batch = (int)p.kblocks_batch;
-  g.splits = p.t.splits;
   g.bias = ep.bias;
   g.act = ep.act;
   g.residual = ep.residual.data != nullptr;
   g.save_z = ep.z.data != nullptr;
   g.stall = g_stall.load(std::memory_order_relaxed);
   g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
-  g.units = p.batches * g.row_tiles * g.col_tiles * g.splits;
+  const long long units = p.t.whole + p.t.rest * p.t.splits;
+  if (units >= 1LL << 31) return VSA_ERR_UNSUPPORTED;
+  g.whole = (int)p.t.whole;
+  g.rest = (int)p.t.rest;
+  g.splits = p.t.splits;
+  g.units = units;
   if (vsa::launch_linear_gemm(g, p.kind, type, sms, st) != cudaSuccess) return VSA_ERR_CUDA;
-  if (!split) return VSA_OK;
+  if (!p.t.rest) return VSA_OK;
   vsa::FinishParams f{};
   f.partial = static_cast<const float*>(workspace);
-  f.splits = p.t.splits;
-  f.batches = (int)p.batches;
-  f.rows = (int)p.rows;
-  f.F = (int)p.cols;
+  f.first = g.whole;
+  f.rest = g.rest;
+  f.splits = g.splits;
+  f.bn = g.bn;
+  f.batches = g.batches;
+  f.row_tiles = g.row_tiles;
+  f.col_tiles = g.col_tiles;
+  f.rows = g.rows;
+  f.F = g.F;
   f.bias = ep.bias;
   f.act = ep.act;
   f.residual = ep.residual;
   f.z = ep.z;
   f.out = ep.out;
-  return vsa::launch_linear_finish(f, type, sms, st) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+  return vsa::launch_linear_finish(f, type, st) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
 }
 
 vsa_status check_weight(const void* w, long long stride, const vsa_linear_sizes* s) {

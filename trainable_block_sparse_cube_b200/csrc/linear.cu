@@ -95,17 +95,40 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 // z s(v) and its slope s + z s (1 - s) v' are silu (v = z) and the tanh form
-// of gelu (v = 2 sqrt(2/pi) (z + 0.044715 z^3)): both keep their relative
-// accuracy where z is far below 0. gelu is z times the normal distribution
-// function, from the complementary error function for the same reason.
+// of gelu (v = 2 sqrt(2/pi) (z + 0.044715 z^3)); both keep their relative
+// accuracy where z is far below 0.
 constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.07135481282805f;  // 2 sqrt(2/pi), that times 0.044715
 
 __device__ __forceinline__ float sigmoid_times(float z, float v) { return __fdividef(z, 1.f + __expf(-v)); }
 
+// gelu is z P(z) with the normal distribution function P. Its tail
+// h = P(-|z|) = exp(-z^2 / 2) t q(t) with t = 1 / (1 + 0.3111 |z|): q is of
+// degree 7, fitted for this to the least relative error over |z| <= 20
+// (1.9e-7; 4.7e-7 as evaluated), so h keeps its accuracy far below 0, at a
+// quarter of the instructions of erfcf (16384 x 1536 x 6144: 341 -> %GELU% us).
+__device__ __forceinline__ float normal_tail(float a, float* density) {
+  const float t = __fdividef(1.f, fmaf(0.3111269772052765f, a, 1.f));
+  const float e = __expf(-0.5f * a * a);
+  float q = 0.03574991226196289f;
+  q = fmaf(q, t, -0.13957644999027252f);
+  q = fmaf(q, t, 0.14943377673625946f);
+  q = fmaf(q, t, -0.011147385463118553f);
+  q = fmaf(q, t, 0.10849696397781372f);
+  q = fmaf(q, t, 0.10846728086471558f);
+  q = fmaf(q, t, 0.12446772307157516f);
+  q = fmaf(q, t, 0.12410826236009598f);
+  *density = e;
+  return q * t * e;
+}
+
 __device__ __forceinline__ float activate(float z, int act) {
   if (act == kActSilu) return sigmoid_times(z, z);
   if (act == kActGeluTanh) return sigmoid_times(z, z * fmaf(kTanhB, z * z, kTanhA));
-  if (act == kActGelu) return 0.5f * z * erfcf(-0.7071067811865476f * z);
+  if (act == kActGelu) {
+    float e;
+    const float a = fminf(fabsf(z), 20.f);  // the tail is 0 beyond: an infinite z meets no 0 x infinity
+    return fmaf(-a, normal_tail(a, &e), z < 0.f ? 0.f : z);
+  }
   return z;
 }
 
@@ -118,8 +141,11 @@ __device__ __forceinline__ float slope(float z, int act) {
     const float s = __fdividef(1.f, 1.f + __expf(-z * fmaf(kTanhB, z * z, kTanhA)));
     return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z * z, kTanhA), s);
   }
-  if (act == kActGelu)  // 1 / sqrt(2 pi)
-    return fmaf(0.3989422804014327f * z, __expf(-0.5f * z * z), 0.5f * erfcf(-0.7071067811865476f * z));
+  if (act == kActGelu) {  // P(z) + z exp(-z^2 / 2) / sqrt(2 pi)
+    float e;
+    const float h = normal_tail(fminf(fabsf(z), 20.f), &e);
+    return fmaf(0.3989422804014327f * z, e, z < 0.f ? h : 1.f - h);
+  }
   return 1.f;
 }
 
@@ -155,20 +181,52 @@ struct Waiter {
   }
 };
 
-// A work unit: one tile of one part of the contraction, neighbours in columns
-// first (the pairs that run together then share their rows of A in L2).
+// Tiles in the order they run in. The pairs that run together take a block of
+// kGroup row tiles by the columns beside it, so that what they load from L2 is
+// few rows of A and few of B (8192^3: 2.25 -> 1.10 GB from DRAM).
+constexpr int kGroup = 8;
+__device__ __forceinline__ void tile_place(int tile, int all_rows, int col_tiles, int* rt, int* ct) {
+  const int group = tile / (kGroup * col_tiles), in = tile - group * kGroup * col_tiles;
+  const int high = min(kGroup, all_rows - group * kGroup);
+  *ct = in / high;
+  *rt = group * kGroup + in - *ct * high;
+}
+
+// A work unit: a tile, or one part of the contraction of a tile of the last
+// round, which has too few tiles for all pairs.
 struct Unit {
-  int batch, row0, col0, split, k0, k1;
-  __device__ __forceinline__ Unit(const GemmParams& p, long long u) {
-    const long long tiles = (long long)p.batches * p.row_tiles * p.col_tiles;
-    split = (int)(u / tiles);
-    const long long t = u - split * tiles;
-    const int rt = (int)(t / p.col_tiles);
-    col0 = (int)(t - (long long)rt * p.col_tiles) * p.bn;
-    batch = rt / p.row_tiles;
+  int batch, row0, col0, part, k0, k1;  // part: index of the partial tile, -1 for a whole contraction
+  __device__ __forceinline__ Unit(const GemmParams& p, unsigned u) {
+    unsigned t = u;
+    part = -1;
+    steps(p, u, &k0, &k1);
+    if (u >= p.whole) {
+      part = u - p.whole;
+      t = p.whole + part % p.rest;
+    }
+    int rt, ct;
+    tile_place(t, p.batches * p.row_tiles, p.col_tiles, &rt, &ct);
+    batch = p.batches > 1 ? rt / p.row_tiles : 0;
     row0 = (rt - batch * p.row_tiles) * 256;
-    k0 = (int)((long long)p.kblocks * split / p.splits);
-    k1 = (int)((long long)p.kblocks * (split + 1) / p.splits);
+    col0 = ct * p.bn;
+  }
+  __device__ __forceinline__ static void steps(const GemmParams& p, unsigned u, int* k0, int* k1) {
+    *k0 = 0;
+    *k1 = p.kblocks;
+    if (u >= p.whole) {
+      const unsigned split = (u - p.whole) / p.rest;
+      *k0 = (int)((unsigned)p.kblocks * split / p.splits);
+      *k1 = (int)((unsigned)p.kblocks * (split + 1) / p.splits);
+    }
+  }
+};
+
+// Stage of the ring and the parity of its use.
+struct Ring {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) stage = 0, parity ^= 1;
   }
 };
 
@@ -182,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   Barriers& sh = *reinterpret_cast<Barriers*>(slots + kEpiWarps * 2 * kSlotBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = (unsigned)p.units;
   const int half = p.bn / 2;  // rows of B in a CTA
   const Waiter wait{p.wait_ns};
 
@@ -210,64 +268,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       // ---- loads of this CTA's operand rows; both CTAs' complete on the even CTA's barriers
       const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : (half + 63) / 64 * 8192;
       const uint32_t pair_bytes = 2 * (kTileA + b_bytes);
-      int it = 0;
+      // Everything the loop over the steps needs is kept up by additions: one
+      // thread issues all loads, and a division costs it more than a load.
+      const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
+      const int b_boxes = (half + 63) / 64;
+      Ring ring;
       bool ok = true;
-      for (long long u = pair; ok && u < p.units; u += pairs) {
+      for (unsigned u = pair; ok && u < units; u += pairs) {
         const Unit w(p, u);
         const int row = w.row0 + (int)rank * 128, col = w.col0 + (int)rank * half;
-        for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-          const int s = it % kStages, use = it / kStages;
-          if (use && !wait(&sh.empty[s], (use - 1) & 1)) {
+        int ch0, ch1, cc0, cc1, bh0, bh1, bc0, bc1;  // kGemmWeight: head and channel of A's and B's boxes
+        int k, kh, kend;                             // channel and head of the step, or row and batch of rows
+        if (KIND == kGemmWeight) {
+          ch0 = row / p.a_d, cc0 = row - ch0 * p.a_d;
+          ch1 = (row + 64) / p.a_d, cc1 = row + 64 - ch1 * p.a_d;
+          bh0 = col / p.b_d, bc0 = col - bh0 * p.b_d;
+          bh1 = (col + 64) / p.b_d, bc1 = col + 64 - bh1 * p.b_d;
+          kh = w.k0 / p.kblocks_batch;
+          k = (w.k0 - kh * p.kblocks_batch) * 64;
+          kend = p.kblocks_batch * 64;
+        } else {
+          kh = w.k0 * 64 / p.a_d;
+          k = w.k0 * 64 - kh * p.a_d;
+          kend = p.a_d;
+        }
+        for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
+          const int s = ring.stage;
+          if (!wait(&sh.empty[s], ring.parity ^ 1)) {  // passes at once where no use came before
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], pair_bytes);
           if (p.stall) continue;
-          const uint32_t bar = mapa(smem_u32(&sh.full[s]), 0);
+          const uint32_t bar = full0 + s * 8;
           const uint32_t a = base + s * kStageBytes, b = a + kTileA;
           if (KIND == kGemmWeight) {
-            const int kbatch = kb / p.kblocks_batch, k = (kb - kbatch * p.kblocks_batch) * 64;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int c = row + 64 * j, h = c / p.a_d;
-              tma_load_4d<2>(a + j * 8192, &p.ta, bar, c - h * p.a_d, k, h, kbatch);
-            }
-            for (int j = 0; j * 64 < half; ++j) {
-              const int c = col + 64 * j, h = c / p.b_d;
-              tma_load_4d<2>(b + j * 8192, &p.tb, bar, c - h * p.b_d, k, h, kbatch);
-            }
+            tma_load_4d<2>(a, &p.ta, bar, cc0, k, ch0, kh);
+            tma_load_4d<2>(b, &p.tb, bar, bc0, k, bh0, kh);
+            tma_load_4d<2>(a + 8192, &p.ta, bar, cc1, k, ch1, kh);
+            if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, bc1, k, bh1, kh);
           } else {
-            const int k = kb * 64, h = k / p.a_d;
-            tma_load_4d<2>(a, &p.ta, bar, k - h * p.a_d, row, h, w.batch);
+            tma_load_4d<2>(a, &p.ta, bar, k, row, kh, w.batch);
             if (KIND == kGemmForward) {
-              tma_load_4d<2>(b, &p.tb, bar, k, col, 0, 0);
+              tma_load_4d<2>(b, &p.tb, bar, kb * 64, col, 0, 0);
             } else {
-              for (int j = 0; j * 64 < half; ++j) tma_load_4d<2>(b + j * 8192, &p.tb, bar, col + 64 * j, k, 0, 0);
+              tma_load_4d<2>(b, &p.tb, bar, col, kb * 64, 0, 0);
+              if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, col + 64, kb * 64, 0, 0);
             }
           }
+          k += 64;
+          if (k >= kend) k = 0, ++kh;
         }
       }
       if (!ok && rank == 0)  // the loads in flight land before the pair's shared memory goes
-        for (int i = it > kStages ? it - kStages : 0; i < it; ++i) mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, p.wait_ns);
+        for (int i = 0; i < kStages; ++i)
+          mbar_wait(&sh.full[i], i < ring.stage ? ring.parity : ring.parity ^ 1, p.wait_ns);
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
       // ---- MMAs of the pair
       const uint32_t idesc = idesc_f16_f32(256, p.bn, KIND == kGemmWeight, KIND != kGemmForward, std::is_same<T, __nv_bfloat16>::value);
       constexpr uint32_t A_STEP = (KIND == kGemmWeight ? 2048 : 32) >> 4, B_STEP = (KIND == kGemmForward ? 32 : 2048) >> 4;
-      int it = 0, tile = 0;
+      Ring ring;
+      int tile = 0;
       bool ok = true;
-      for (long long u = pair; ok && u < p.units; u += pairs, ++tile) {
-        const Unit w(p, u);
+      for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
+        int k0, k1;
+        Unit::steps(p, u, &k0, &k1);
         const int buf = tile & 1, use = tile >> 1;
         if (use && !wait.pair(&sh.acc_empty[buf], (use - 1) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        for (int kb = w.k0; kb < w.k1; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!wait(&sh.full[s], (it / kStages) & 1)) {
+        for (int kb = k0; kb < k1; ++kb, ring.next()) {
+          const int s = ring.stage;
+          if (!wait(&sh.full[s], ring.parity)) {
             ok = false;
             break;
           }
@@ -277,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
           const uint64_t bd = sdesc_sw128(a + kTileA, KIND == kGemmForward ? 16 : 8192, 1024);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma_f16_ss_pair(tmem + buf * kAccColumns, ad + i * A_STEP, bd + i * B_STEP, idesc, kb > w.k0 || i);
+            mma_f16_ss_pair(tmem + buf * kAccColumns, ad + i * A_STEP, bd + i * B_STEP, idesc, kb > k0 || i);
           mma_commit_pair(&sh.empty[s]);
         }
         if (ok) mma_commit_pair(&sh.acc_full[buf]);
@@ -297,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     int tile = 0, flip = 0;
     uint32_t res_phase = 0;
     bool ok = true;
-    for (long long u = pair; ok && u < p.units; u += pairs, ++tile) {
+    for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
       const Unit w(p, u);
       const int buf = tile & 1;
       if (!__all_sync(0xffffffffu, wait(&sh.acc_full[buf], (tile >> 1) & 1))) break;
@@ -305,12 +381,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       const int row = w.row0 + (int)rank * 128 + quarter * 32;
       for (int g = ew >> 2; g * 64 < p.bn; g += 2) {
         const int col = w.col0 + g * 64;
-        if (row >= p.rows || col >= p.F) break;
         const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 64);
-        if (p.splits > 1) {
+        if (row >= p.rows || col >= p.F) break;
+        if (w.part >= 0) {
           // a part of the contraction: fp32 sums, 32 columns a store
 #pragma unroll 1
-          for (int h = 0; h < 2 && col + 32 * h < p.F; ++h, flip ^= 1) {
+          for (int h = 0; h < 2; ++h, flip ^= 1) {
             uint32_t r[32];
             tmem_ld32(acc + 32 * h, r);
             if (lane == 0) bulk_wait_read<1>();
@@ -323,7 +399,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_4d(&p.tout, slot0_addr + flip * kSlotBytes, col + 32 * h, row, w.batch, w.split);
+              tma_store_2d(&p.tpart, slot0_addr + flip * kSlotBytes, g * 64 + 32 * h,
+                           w.part * 256 + (int)rank * 128 + quarter * 32);
               bulk_commit();
             }
           }
@@ -393,35 +470,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
 }
 
 // ---------------------------------------------------------------- split contractions
-// out = act(sum of the parts + bias) + residual, 8 columns a thread.
+// out = act(sum of the parts + bias) + residual of the split tiles, 8 columns a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
-  const int groups = p.F / 8;
-  const long long n8 = (long long)p.batches * p.rows * groups, part = (long long)p.batches * p.rows * p.F;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += (long long)gridDim.x * blockDim.x) {
-    const long long m = i / groups;
-    const int c = (int)(i - m * groups) * 8;
-    const int b = (int)(m / p.rows), n = (int)(m - (long long)b * p.rows);
-    const float* src = p.partial + m * p.F + c;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int groups = p.bn / 8, per_tile = 256 * groups;
+  const int tile = blockIdx.x / (per_tile / 256), in = (blockIdx.x % (per_tile / 256)) * 256 + threadIdx.x;
+  int rt, ct;
+  tile_place(p.first + tile, p.batches * p.row_tiles, p.col_tiles, &rt, &ct);
+  const int b = rt / p.row_tiles, r = in / groups, cc = (in - r * groups) * 8;
+  const int n = (rt - b * p.row_tiles) * 256 + r, c = ct * p.bn + cc;
+  if (n >= p.rows || c >= p.F) return;
+  const float* src = p.partial + ((long long)tile * 256 + r) * p.bn + cc;
+  const long long part = (long long)p.rest * 256 * p.bn;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(src + s * part));
-      const float4 y = __ldcs(reinterpret_cast<const float4*>(src + s * part) + 1);
-      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-    }
-    if (p.bias) add_bias8(v, p.bias + c);
-    if (p.z.data) *reinterpret_cast<uint4*>(at<T>(p.z, b, n, c)) = pack8<T>(v);
-    activate8(v, p.act);
-    if (p.residual.data) {
-      float x[8];
-      unpack8<T>(*reinterpret_cast<const uint4*>(at<T>(p.residual, b, n, c)), x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += x[k];
-    }
-    *reinterpret_cast<uint4*>(at<T>(p.out, b, n, c)) = pack8<T>(v);
+  for (int s = 0; s < p.splits; ++s) {
+    const float4 x = __ldcs(reinterpret_cast<const float4*>(src + s * part));
+    const float4 y = __ldcs(reinterpret_cast<const float4*>(src + s * part) + 1);
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
   }
+  if (p.bias) add_bias8(v, p.bias + c);
+  if (p.z.data) *reinterpret_cast<uint4*>(at<T>(p.z, b, n, c)) = pack8<T>(v);
+  activate8(v, p.act);
+  if (p.residual.data) {
+    float x[8];
+    unpack8<T>(*reinterpret_cast<const uint4*>(at<T>(p.residual, b, n, c)), x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += x[k];
+  }
+  *reinterpret_cast<uint4*>(at<T>(p.out, b, n, c)) = pack8<T>(v);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -588,9 +666,8 @@ cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_
   return type ? launch_gemm_kind<__half>(p, kind, num_sms, st) : launch_gemm_kind<__nv_bfloat16>(p, kind, num_sms, st);
 }
 
-cudaError_t launch_linear_finish(const FinishParams& p, int type, int num_sms, cudaStream_t st) {
-  const long long blocks = ((long long)p.batches * p.rows * (p.F / 8) + 255) / 256, most = 8LL * num_sms;
-  const int grid = (int)(blocks < most ? blocks : most);
+cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t st) {
+  const int grid = p.rest * (p.bn / 8);
   if (type) finish_kernel<__half><<<grid, 256, 0, st>>>(p);
   else finish_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();

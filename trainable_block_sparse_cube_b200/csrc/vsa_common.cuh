@@ -205,6 +205,7 @@ struct RowsView {
 // its channels, an MN-major one along its rows.
 struct GemmParams {
   CUtensorMap ta, tb, tout, tres, tz;
+  CUtensorMap tpart;        // fp32 parts of split tiles: rows (part, row of the tile) of bn, 32 x 32 boxes
   int a_d, b_d, o_d;        // channels of a head of A, B, out
   int bn;                   // columns of a tile: 128, 192 or 256
   int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
@@ -212,18 +213,18 @@ struct GemmParams {
   int F, col_tiles;         // columns
   int kblocks;              // 64-long blocks of the contraction
   int kblocks_batch;        // kGemmWeight: blocks of a batch of rows
-  int splits;               // > 1: tout is fp32 [splits, batches, rows, F] (32-column boxes), see FinishParams
+  int whole, rest, splits;  // tiles computed in one go, and those computed in parts of the contraction
   const float* bias;        // [F] or null
   int act, residual, save_z;
   int stall;                // test hook: no operand is loaded
   unsigned long long wait_ns;
-  long long units;          // tiles x splits
+  long long units;          // whole + rest x splits
 };
 
-// Sums the parts of a split contraction and applies the epilogue.
+// Sums the parts of the split tiles (number first, first + 1, ...) and applies the epilogue.
 struct FinishParams {
-  const float* partial;
-  int splits, batches, rows, F;
+  const float* partial;     // [splits, rest, 256, bn]
+  int first, rest, splits, bn, batches, row_tiles, col_tiles, rows, F;
   const float* bias;
   int act;
   RowsView residual, z, out;   // data null: none
@@ -250,7 +251,7 @@ enum : int { kGemmForward = 0, kGemmInput = 1, kGemmWeight = 2 };
 constexpr int kSkinnyRows = 8;
 // type: 0 bf16, 1 fp16
 cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_sms, cudaStream_t st);
-cudaError_t launch_linear_finish(const FinishParams& p, int type, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t st);
 cudaError_t launch_linear_skinny(const SkinnyParams& p, int type, cudaStream_t st);
 cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaStream_t st);
 // Reads and clears the current device's error word of the linear kernels (synchronises the stream).

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -75,7 +76,14 @@ class LinearSizes(ctypes.Structure):
                 ("F", ctypes.c_int)]
 
 
+# The same structs as bytes: packing one costs a tenth of filling a ctypes structure.
+_pack_heads = struct.Struct("@Piqqq").pack
+_pack_positions = struct.Struct("@6iPiq").pack
+_pack_rope_sizes = struct.Struct("@4i").pack
+_pack_linear_sizes = struct.Struct("@5i").pack
+
 _lib = None
+_projection = None
 
 
 def load():
@@ -163,6 +171,29 @@ def load():
     return L
 
 
+def _load_projection():
+    """The projection side's functions with untyped pointers, to be called with packed structs."""
+    global _projection
+    if _projection is None:
+        load()
+        L = ctypes.CDLL(lib_path)
+        vp, i32, sz, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+        for name, args in (("vsa_rope", [vp] * 8), ("vsa_rope_backward", [vp] * 8),
+                           ("vsa_qk_norm_rope", [vp] * 7 + [ctypes.c_float] + [vp] * 3),
+                           ("vsa_qk_norm_rope_backward", [vp] * 7 + [ctypes.c_float] + [vp] * 7 + [sz, vp]),
+                           ("vsa_linear", [vp] * 3 + [i64, vp, i32] + [vp] * 4 + [sz, vp]),
+                           ("vsa_linear_backward", [vp] * 3 + [i64, vp, i32] + [vp] * 5 + [sz, vp])):
+            getattr(L, name).argtypes = args
+        L.vsa_qk_norm_rope_backward_workspace_bytes.argtypes = [i32]
+        L.vsa_linear_workspace_bytes.argtypes = [vp]
+        L.vsa_linear_backward_workspace_bytes.argtypes = [vp, i32]
+        for name in ("vsa_qk_norm_rope_backward_workspace_bytes", "vsa_linear_workspace_bytes",
+                     "vsa_linear_backward_workspace_bytes"):
+            getattr(L, name).restype = sz
+        _projection = L
+    return _projection
+
+
 def _check(code: int, what: str):
     if code != 0:
         raise VSAError(code, what)
@@ -173,7 +204,8 @@ def _ptr(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # what torch.cuda.current_stream().cuda_stream gives, without building the Stream object (3 us)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, name, dtype, shape):
@@ -443,6 +475,7 @@ class Rotation:
                 self.spec.axis[j] = a
                 self.spec.freq[j] = scale[a] * float(base) ** (-2.0 * j / self.rot if shared else -2.0 * i / n)
                 j += 1
+        self._packed = bytes(self.spec)
 
 
 class _OnDevice:
@@ -452,7 +485,7 @@ class _OnDevice:
         self.device, self.before = device.index, None
 
     def __enter__(self):
-        now = torch.cuda.current_device()
+        now = torch._C._cuda_getDevice()
         if now != self.device:
             self.before = now
             torch.cuda.set_device(self.device)
@@ -479,7 +512,10 @@ def _need_heads(t, name, like=None, dtype=None, device=None):
 
 
 def _heads(t):
-    return None if t is None else ctypes.byref(Heads(t.data_ptr(), t.shape[1], t.stride(0), t.stride(1), t.stride(2)))
+    if t is None:
+        return None
+    s = t.stride()
+    return _pack_heads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
 
 
 def _where(rotation, grid, origin, positions, B, N, device):
@@ -492,7 +528,7 @@ def _where(rotation, grid, origin, positions, B, N, device):
             raise ValueError("origin must fit into 32 bits")
         if N != grid[0] * grid[1] * grid[2]:
             raise ValueError(f"N = {N} must equal T*H*W of grid {tuple(grid)}")
-        return Positions(grid[0], grid[1], grid[2], (ctypes.c_int * 3)(*origin), None, 0, 0)
+        return _pack_positions(*grid, *origin, 0, 0, 0)
     p = positions
     if not isinstance(p, torch.Tensor) or not p.is_cuda or p.device != device:
         raise ValueError(f"positions must be a CUDA tensor on {device}")
@@ -505,8 +541,8 @@ def _where(rotation, grid, origin, positions, B, N, device):
                          f"got {tuple(positions.shape)}")
     if p.numel() and not p[0].is_contiguous():
         raise ValueError("positions must be contiguous")
-    return Positions(0, 0, 0, (ctypes.c_int * 3)(), p.data_ptr() if p.numel() else 16,
-                     0 if p.dtype == torch.int32 else 1, p.stride(0) if p.shape[0] > 1 else 0)
+    return _pack_positions(0, 0, 0, 0, 0, 0, p.data_ptr() if p.numel() else 16, 0 if p.dtype == torch.int32 else 1,
+                           p.stride(0) if p.shape[0] > 1 else 0)
 
 
 def _sizes(q, k, rotation, names=("q", "k")):
@@ -518,7 +554,7 @@ def _sizes(q, k, rotation, names=("q", "k")):
         _need_heads(k, names[1], dtype=q.dtype, device=q.device)
         if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, D):
             raise ValueError(f"{names[1]} must have shape [{B}, heads, {N}, {D}], got {tuple(k.shape)}")
-    return RopeSizes(TYPES[q.dtype], B, N, D)
+    return B, N, D, _pack_rope_sizes(TYPES[q.dtype], B, N, D)
 
 
 def _need_weight(w, name, D, device):
@@ -536,7 +572,7 @@ def _outputs(q, k, q_out, k_out, names, like_input=False):
             if o is not None:
                 raise ValueError(f"{name} has no input")
         elif o is None:
-            o = torch.empty_like(t) if like_input else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            o = torch.empty_like(t) if like_input else torch.empty_like(t, memory_format=torch.contiguous_format)
         else:
             _need_heads(o, name, like=t.shape, dtype=t.dtype, device=t.device)
         out.append(o)
@@ -548,24 +584,24 @@ def rope(q, k, rotation, grid=None, origin=(0, 0, 0), positions=None, q_out=None
     another number of heads). Tokens lie on the raster ``grid`` (T, H, W) from ``origin`` on, or at
     ``positions`` ([N, axes] or [B, N, axes], int32 or float32). Returns (q_out, k_out), contiguous unless
     given; an output may be its input. Enqueued on the current stream."""
-    sizes = _sizes(q, k, rotation)
-    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, q.device)
+    B, N, D, sizes = _sizes(q, k, rotation)
+    where = _where(rotation, grid, origin, positions, B, N, q.device)
     with _OnDevice(q.device):
         q_out, k_out = _outputs(q, k, q_out, k_out, ("q_out", "k_out"))
-        _check(load().vsa_rope(sizes, rotation.spec, where, _heads(q), _heads(k), _heads(q_out), _heads(k_out),
-                               _stream()), "vsa_rope")
+        _check(_load_projection().vsa_rope(sizes, rotation._packed, where, _heads(q), _heads(k), _heads(q_out),
+                                           _heads(k_out), _stream()), "vsa_rope")
     return q_out, k_out
 
 
 def rope_backward(dq_out, dk_out, rotation, grid=None, origin=(0, 0, 0), positions=None, dq=None, dk=None):
     """Gradients of rope's inputs from those of its outputs (dk_out may be None): (dq, dk), contiguous unless
     given. Enqueued on the current stream."""
-    sizes = _sizes(dq_out, dk_out, rotation, ("dq_out", "dk_out"))
-    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, dq_out.device)
+    B, N, _, sizes = _sizes(dq_out, dk_out, rotation, ("dq_out", "dk_out"))
+    where = _where(rotation, grid, origin, positions, B, N, dq_out.device)
     with _OnDevice(dq_out.device):
         dq, dk = _outputs(dq_out, dk_out, dq, dk, ("dq", "dk"))
-        _check(load().vsa_rope_backward(sizes, rotation.spec, where, _heads(dq_out), _heads(dk_out), _heads(dq),
-                                        _heads(dk), _stream()), "vsa_rope_backward")
+        _check(_load_projection().vsa_rope_backward(sizes, rotation._packed, where, _heads(dq_out), _heads(dk_out),
+                                                    _heads(dq), _heads(dk), _stream()), "vsa_rope_backward")
     return dq, dk
 
 
@@ -573,15 +609,15 @@ def qk_norm_rope(q, k, q_weight, k_weight, rotation, grid=None, origin=(0, 0, 0)
                  q_out=None, k_out=None):
     """RMS norm of every head's queries and keys (weights [D] fp32 or None) and the rotation of ``rope`` in one
     pass; arguments, outputs and stream as there."""
-    sizes = _sizes(q, k, rotation)
-    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, q.device)
-    _need_weight(q_weight, "q_weight", sizes.D, q.device)
-    _need_weight(k_weight, "k_weight", sizes.D, q.device)
+    B, N, D, sizes = _sizes(q, k, rotation)
+    where = _where(rotation, grid, origin, positions, B, N, q.device)
+    _need_weight(q_weight, "q_weight", D, q.device)
+    _need_weight(k_weight, "k_weight", D, q.device)
     with _OnDevice(q.device):
         q_out, k_out = _outputs(q, k, q_out, k_out, ("q_out", "k_out"))
-        _check(load().vsa_qk_norm_rope(sizes, rotation.spec, where, _heads(q), _heads(k), _ptr(q_weight),
-                                       _ptr(k_weight), eps, _heads(q_out), _heads(k_out), _stream()),
-               "vsa_qk_norm_rope")
+        _check(_load_projection().vsa_qk_norm_rope(sizes, rotation._packed, where, _heads(q), _heads(k),
+                                                   _ptr(q_weight), _ptr(k_weight), eps, _heads(q_out),
+                                                   _heads(k_out), _stream()), "vsa_qk_norm_rope")
     return q_out, k_out
 
 
@@ -590,23 +626,23 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, rotation, gr
     """Gradients of qk_norm_rope from its inputs (nothing is saved) and the gradients of its outputs. Returns
     (dq, dk, dq_weight, dk_weight): dq and dk in the order of dimensions that q and k are stored in unless
     given, the weights' in fp32 (None where the weight is None). Enqueued on the current stream."""
-    sizes = _sizes(q, k, rotation)
-    where = _where(rotation, grid, origin, positions, sizes.B, sizes.N, q.device)
-    _need_weight(q_weight, "q_weight", sizes.D, q.device)
-    _need_weight(k_weight, "k_weight", sizes.D, q.device)
+    B, N, D, sizes = _sizes(q, k, rotation)
+    where = _where(rotation, grid, origin, positions, B, N, q.device)
+    _need_weight(q_weight, "q_weight", D, q.device)
+    _need_weight(k_weight, "k_weight", D, q.device)
     _need_heads(dq_out, "dq_out", like=q.shape, dtype=q.dtype, device=q.device)
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out must be given together")
     if k is not None:
         _need_heads(dk_out, "dk_out", like=k.shape, dtype=q.dtype, device=q.device)
     with _OnDevice(q.device):
-        L = load()
+        L = _load_projection()
         dq, dk = _outputs(q, k, dq, dk, ("dq", "dk"), like_input=True)
         dwq = None if q_weight is None else torch.empty_like(q_weight)
         dwk = None if k is None or k_weight is None else torch.empty_like(k_weight)
-        nb = L.vsa_qk_norm_rope_backward_workspace_bytes(sizes.D)
+        nb = L.vsa_qk_norm_rope_backward_workspace_bytes(D)
         ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
-        _check(L.vsa_qk_norm_rope_backward(sizes, rotation.spec, where, _heads(q), _heads(k), _ptr(q_weight),
+        _check(L.vsa_qk_norm_rope_backward(sizes, rotation._packed, where, _heads(q), _heads(k), _ptr(q_weight),
                                            _ptr(k_weight), eps, _heads(dq_out), _heads(dk_out), _heads(dq), _heads(dk),
                                            _ptr(dwq), _ptr(dwk), _ptr(ws), nb, _stream()),
                "vsa_qk_norm_rope_backward")
@@ -634,8 +670,8 @@ def _rows(t):
         return None
     s = t.stride()
     if len(s) == 3:
-        return Heads(t.data_ptr(), 1, s[0], 0, s[1])
-    return Heads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
+        return _pack_heads(t.data_ptr(), 1, s[0], 0, s[1])
+    return _pack_heads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
 
 
 def _linear_sizes(x, weight, activation):
@@ -652,7 +688,7 @@ def _linear_sizes(x, weight, activation):
         raise ValueError("weight must have contiguous rows")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    return LinearSizes(TYPES[x.dtype], B, N, K, weight.shape[0])
+    return B, N, weight.shape[0], _pack_linear_sizes(TYPES[x.dtype], B, N, K, weight.shape[0])
 
 
 def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out=None, z=None):
@@ -662,23 +698,23 @@ def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out
     [B, heads, N, F / heads] if ``heads`` is given; ``residual``, ``out`` and ``z`` (which receives
     x weight^T + bias for linear_backward) have that shape. out may be the residual. Enqueued on the current
     stream."""
-    sizes = _linear_sizes(x, weight, activation)
-    device, F = x.device, sizes.F
+    B, N, F, sizes = _linear_sizes(x, weight, activation)
+    device = x.device
     if bias is not None:
         _need_weight(bias, "bias", F, device)
     if heads is None:
-        shape = torch.Size((sizes.B, sizes.N, F))
+        shape = torch.Size((B, N, F))
     elif heads < 1 or F % heads:
         raise ValueError(f"{F} channels do not split into {heads} heads")
     else:
-        shape = torch.Size((sizes.B, heads, sizes.N, F // heads))
+        shape = torch.Size((B, heads, N, F // heads))
     for t, name in ((residual, "residual"), (out, "out"), (z, "z")):
         if t is not None:
             _need_rows(t, name, x.dtype, device, shape)
     with _OnDevice(device):
-        L = load()
+        L = _load_projection()
         if out is None:
-            out = torch.empty(shape, dtype=x.dtype, device=device)
+            out = x.new_empty(shape)
         nb = L.vsa_linear_workspace_bytes(sizes)
         ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
         _check(L.vsa_linear(sizes, _rows(x), weight.data_ptr(), weight.stride(0), _ptr(bias), ACTIVATIONS[activation],
@@ -691,22 +727,22 @@ def linear_backward(x, weight, dout, z=None, activation=None, bias=False, dx=Non
     stored, needed with an activation; dbias (fp32) is None unless ``bias``; ``want`` switches dx and dweight
     off. dx is in the order of dimensions that x is stored in unless given. The residual's gradient is dout.
     Enqueued on the current stream."""
-    sizes = _linear_sizes(x, weight, activation)
-    device, F = x.device, sizes.F
+    B, N, F, sizes = _linear_sizes(x, weight, activation)
+    device = x.device
     _need_rows(dout, "dout", x.dtype, device)
     s = dout.shape
-    if (s if len(s) == 3 else (s[0], s[2], s[1] * s[3])) != (sizes.B, sizes.N, F):
-        raise ValueError(f"dout must have shape [{sizes.B}, {sizes.N}, {F}] or [{sizes.B}, heads, {sizes.N}, D], "
+    if (s if len(s) == 3 else (s[0], s[2], s[1] * s[3])) != (B, N, F):
+        raise ValueError(f"dout must have shape [{B}, {N}, {F}] or [{B}, heads, {N}, D], "
                          f"got {tuple(s)}")
     if activation is not None:
         _need_rows(z, "z", x.dtype, device, s)
     if dx is not None:
         _need_rows(dx, "dx", x.dtype, device, x.shape)
     with _OnDevice(device):
-        L = load()
+        L = _load_projection()
         if want[0] and dx is None:
             dx = torch.empty_like(x)
-        dw = torch.empty(weight.shape, dtype=x.dtype, device=device) if want[1] else None
+        dw = torch.empty_like(weight, memory_format=torch.contiguous_format) if want[1] else None
         db = torch.empty(F, dtype=torch.float32, device=device) if bias else None
         nb = L.vsa_linear_backward_workspace_bytes(sizes, ACTIVATIONS[activation])
         ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
