@@ -13,7 +13,7 @@
 //    (cta_group::2) reads both halves, so a CTA loads 16 + bn/16 KB a 64-long
 //    step of the contraction instead of the 16 + bn/8 KB of a lone CTA: the
 //    L2 -> SM rate, not the tensor cores, would bound the latter. One thread
-//    issues the loads (5 stages of 32 KB), one the MMAs, eight warps the
+//    issues the loads (6 stages of 32 KB), one the MMAs, eight warps the
 //    epilogue of the tile before (two accumulators of up to 256 columns fill
 //    the SM's tensor memory). Bound by the tensor cores where the product is
 //    large.
@@ -41,7 +41,7 @@ using namespace ptx;
 
 __device__ int g_linear_error;
 
-constexpr int kStages = 5, kStageBytes = 32768, kTileA = 16384;
+constexpr int kStages = 6, kStageBytes = 32768, kTileA = 16384;
 constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
 constexpr int kSlotBytes = 4096;  // 32 rows of 128 bytes
 constexpr int kAccColumns = 256;
@@ -53,7 +53,7 @@ struct Barriers {
   uint64_t drained;
   uint32_t tmem;
 };
-constexpr int kGemmSmem = 1024 + kStages * kStageBytes + kEpiWarps * 2 * kSlotBytes + (int)sizeof(Barriers);
+constexpr int kGemmSmem = 1024 + kStages * kStageBytes + kEpiWarps * kSlotBytes + (int)sizeof(Barriers);
 static_assert(kGemmSmem <= 227 * 1024, "shared memory");
 
 // ---------------------------------------------------------------- arithmetic
@@ -189,13 +189,14 @@ __device__ __forceinline__ T* at(const RowsView& v, int b, int n, int c) {
 }
 
 // ---------------------------------------------------------------- tensor cores
+// Bounded waits; a warp's lanes give up together.
 struct Waiter {
   unsigned long long limit;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    return mbar_wait(bar, parity, limit) || gave_up();
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)) || gave_up();
   }
   __device__ __forceinline__ bool pair(uint64_t* bar, uint32_t parity) const {  // arrivals of both CTAs
-    return mbar_wait_cluster(bar, parity, limit) || gave_up();
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit)) || gave_up();
   }
   __device__ __forceinline__ static bool gave_up() {
     atomicOr(&g_linear_error, kErrTimeout);
@@ -259,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* const slots = raw + (base - smem_u32(raw)) + kStages * kStageBytes;
-  Barriers& sh = *reinterpret_cast<Barriers*>(slots + kEpiWarps * 2 * kSlotBytes);
+  Barriers& sh = *reinterpret_cast<Barriers*>(slots + kEpiWarps * kSlotBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = (unsigned)p.units;
@@ -285,72 +286,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
+  // The two issuing warps run their loops as whole warps, so that what they
+  // compute is uniform, and elect a lane to issue.
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- loads of this CTA's operand rows; both CTAs' complete on the even CTA's barriers
-      const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : (half + 63) / 64 * 8192;
-      const uint32_t pair_bytes = 2 * (kTileA + b_bytes);
-      // Everything the loop over the steps needs is kept up by additions: one
-      // thread issues all loads, and a division costs it more than a load.
-      const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
-      const int b_boxes = (half + 63) / 64;
-      Ring ring;
-      bool ok = true;
-      for (unsigned u = pair; ok && u < units; u += pairs) {
-        const Unit w(p, u);
-        const int row = w.row0 + (int)rank * 128, col = w.col0 + (int)rank * half;
-        int ch0, ch1, cc0, cc1, bh0, bh1, bc0, bc1;  // kGemmWeight: head and channel of A's and B's boxes
-        int k, kh, kend;                             // channel and head of the step, or row and batch of rows
-        if (KIND == kGemmWeight) {
-          ch0 = row / p.a_d, cc0 = row - ch0 * p.a_d;
-          ch1 = (row + 64) / p.a_d, cc1 = row + 64 - ch1 * p.a_d;
-          bh0 = col / p.b_d, bc0 = col - bh0 * p.b_d;
-          bh1 = (col + 64) / p.b_d, bc1 = col + 64 - bh1 * p.b_d;
-          kh = w.k0 / p.kblocks_batch;
-          k = (w.k0 - kh * p.kblocks_batch) * 64;
-          kend = p.kblocks_batch * 64;
-        } else {
-          kh = w.k0 * 64 / p.a_d;
-          k = w.k0 * 64 - kh * p.a_d;
-          kend = p.a_d;
-        }
-        for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
-          const int s = ring.stage;
-          if (!wait(&sh.empty[s], ring.parity ^ 1)) {  // passes at once where no use came before
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], pair_bytes);
-          if (p.stall) continue;
+    // ---- loads of this CTA's operand rows; both CTAs' complete on the even CTA's barriers
+    const int b_boxes = (half + 63) / 64;
+    const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : b_boxes * 8192;
+    const uint32_t pair_bytes = 2 * (kTileA + b_bytes);
+    const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
+    const bool load = p.stall == 0;
+    Ring ring;
+    bool ok = true;
+    for (unsigned u = pair; ok && u < units; u += pairs) {
+      // Divisions here; the steps keep their coordinates up by additions (a
+      // division costs the issuing warp more than a load).
+      const Unit w(p, u);
+      const int row = w.row0 + (int)rank * 128, col = w.col0 + (int)rank * half;
+      int ch0, ch1, cc0, cc1, bh0, bh1, bc0, bc1;  // kGemmWeight: head and channel of A's and B's boxes
+      int k, kh, kend;                             // channel and head of the step, or row and batch of rows
+      if (KIND == kGemmWeight) {
+        ch0 = row / p.a_d, cc0 = row - ch0 * p.a_d;
+        ch1 = (row + 64) / p.a_d, cc1 = row + 64 - ch1 * p.a_d;
+        bh0 = col / p.b_d, bc0 = col - bh0 * p.b_d;
+        bh1 = (col + 64) / p.b_d, bc1 = col + 64 - bh1 * p.b_d;
+        kh = w.k0 / p.kblocks_batch;
+        k = (w.k0 - kh * p.kblocks_batch) * 64;
+        kend = p.kblocks_batch * 64;
+      } else {
+        kh = w.k0 * 64 / p.a_d;
+        k = w.k0 * 64 - kh * p.a_d;
+        kend = p.a_d;
+      }
+      for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
+        const int s = ring.stage;
+        ok = wait.warp(&sh.empty[s], ring.parity ^ 1);  // passes at once where no use came before
+        if (!ok) break;
+        if (elect_one()) {
           const uint32_t bar = full0 + s * 8;
           const uint32_t a = base + s * kStageBytes, b = a + kTileA;
-          if (KIND == kGemmWeight) {
-            tma_load_4d<2>(a, &p.ta, bar, cc0, k, ch0, kh);
-            tma_load_4d<2>(b, &p.tb, bar, bc0, k, bh0, kh);
-            tma_load_4d<2>(a + 8192, &p.ta, bar, cc1, k, ch1, kh);
-            if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, bc1, k, bh1, kh);
-          } else {
-            tma_load_4d<2>(a, &p.ta, bar, k, row, kh, w.batch);
-            if (KIND == kGemmForward) {
-              tma_load_4d<2>(b, &p.tb, bar, kb * 64, col, 0, 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], pair_bytes);
+          if (load) {
+            if (KIND == kGemmWeight) {
+              tma_load_4d<2>(a, &p.ta, bar, cc0, k, ch0, kh);
+              tma_load_4d<2>(b, &p.tb, bar, bc0, k, bh0, kh);
+              tma_load_4d<2>(a + 8192, &p.ta, bar, cc1, k, ch1, kh);
+              if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, bc1, k, bh1, kh);
             } else {
-              tma_load_4d<2>(b, &p.tb, bar, col, kb * 64, 0, 0);
-              if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, col + 64, kb * 64, 0, 0);
+              tma_load_4d<2>(a, &p.ta, bar, k, row, kh, w.batch);
+              if (KIND == kGemmForward) {
+                tma_load_4d<2>(b, &p.tb, bar, kb * 64, col, 0, 0);
+              } else {
+                tma_load_4d<2>(b, &p.tb, bar, col, kb * 64, 0, 0);
+                if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, col + 64, kb * 64, 0, 0);
+              }
             }
           }
-          k += 64;
-          if (k >= kend) k = 0, ++kh;
         }
+        k += 64;
+        if (k >= kend) k = 0, ++kh;
       }
-      if (!ok && rank == 0)  // the loads in flight land before the pair's shared memory goes
-        for (int i = 0; i < kStages; ++i)
-          mbar_wait(&sh.full[i], i < ring.stage ? ring.parity : ring.parity ^ 1, p.wait_ns);
     }
+    if (!ok && rank == 0)  // the loads in flight land before the pair's shared memory goes
+      for (int i = 0; i < kStages; ++i)
+        mbar_wait(&sh.full[i], i < ring.stage ? ring.parity : ring.parity ^ 1, p.wait_ns);
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       // ---- MMAs of the pair
-      const uint32_t idesc = idesc_f16_f32(256, p.bn, KIND == kGemmWeight, KIND != kGemmForward, std::is_same<T, __nv_bfloat16>::value);
+      const uint32_t idesc =
+          idesc_f16_f32(256, p.bn, KIND == kGemmWeight, KIND != kGemmForward, std::is_same<T, __nv_bfloat16>::value);
       constexpr uint32_t A_STEP = (KIND == kGemmWeight ? 2048 : 32) >> 4, B_STEP = (KIND == kGemmForward ? 32 : 2048) >> 4;
+      const uint64_t ad0 = sdesc_sw128(base, KIND == kGemmWeight ? 8192 : 16, 1024);
+      const uint64_t bd0 = sdesc_sw128(base + kTileA, KIND == kGemmForward ? 16 : 8192, 1024);
       Ring ring;
       int tile = 0;
       bool ok = true;
@@ -358,47 +364,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         int k0, k1;
         Unit::steps(p, u, &k0, &k1);
         const int buf = tile & 1, use = tile >> 1;
-        if (use && !wait.pair(&sh.acc_empty[buf], (use - 1) & 1)) {
-          ok = false;
-          break;
-        }
+        const uint32_t acc = tmem + buf * kAccColumns;
+        ok = !use || wait.pair(&sh.acc_empty[buf], (use - 1) & 1);
+        if (!ok) break;
         tc_fence_after();
+        uint32_t add = 0;
         for (int kb = k0; kb < k1; ++kb, ring.next()) {
           const int s = ring.stage;
-          if (!wait(&sh.full[s], ring.parity)) {
-            ok = false;
-            break;
-          }
+          ok = wait.warp(&sh.full[s], ring.parity);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = base + s * kStageBytes;
-          const uint64_t ad = sdesc_sw128(a, KIND == kGemmWeight ? 8192 : 16, 1024);
-          const uint64_t bd = sdesc_sw128(a + kTileA, KIND == kGemmForward ? 16 : 8192, 1024);
+          if (elect_one()) {
+            const uint64_t ad = ad0 + (uint64_t)(s * (kStageBytes >> 4)), bd = bd0 + (uint64_t)(s * (kStageBytes >> 4));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_f16_ss_pair(tmem + buf * kAccColumns, ad + i * A_STEP, bd + i * B_STEP, idesc, kb > k0 || i);
-          mma_commit_pair(&sh.empty[s]);
+            for (int i = 0; i < 4; ++i) mma_f16_ss_pair(acc, ad + i * A_STEP, bd + i * B_STEP, idesc, i ? 1u : add);
+            mma_commit_pair(&sh.empty[s]);
+            if (kb + 1 == k1) mma_commit_pair(&sh.acc_full[buf]);
+          }
+          add = 1;
         }
-        if (ok) mma_commit_pair(&sh.acc_full[buf]);
       }
       if (!ok) {  // the MMAs in flight end before the tensor memory goes
-        mma_commit_pair(&sh.drained);
+        if (elect_one()) mma_commit_pair(&sh.drained);
         mbar_wait(&sh.drained, 0, p.wait_ns);
       }
     }
   } else {
-    // ---- epilogue: a warp takes 32 rows and every second 64-column group of the tile
+    // ---- epilogue: a warp takes 32 rows and every second 64-column group of the
+    // tile, through a slot of 32 swizzled 128-byte rows
     const int ew = warp - 2, quarter = warp & 3;
-    uint8_t* const slot0 = slots + ew * 2 * kSlotBytes;
-    const uint32_t slot0_addr = smem_u32(slot0);
+    uint8_t* const mine = slots + ew * kSlotBytes + lane * 128;
+    const uint32_t slot = smem_u32(slots + ew * kSlotBytes);
     const int sw = lane & 7;
-    const uint32_t lane_off = lane * 128;
-    int tile = 0, flip = 0;
+    int tile = 0;
     uint32_t res_phase = 0;
     bool ok = true;
     for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
       const Unit w(p, u);
       const int buf = tile & 1;
-      if (!__all_sync(0xffffffffu, wait(&sh.acc_full[buf], (tile >> 1) & 1))) break;
+      if (!wait.warp(&sh.acc_full[buf], (tile >> 1) & 1)) break;
       tc_fence_after();
       const int row = w.row0 + (int)rank * 128 + quarter * 32;
       for (int g = ew >> 2; g * 64 < p.bn; g += 2) {
@@ -408,75 +412,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         if (w.part >= 0) {
           // a part of the contraction: fp32 sums, 32 columns a store
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h, flip ^= 1) {
+          for (int h = 0; h < 2; ++h) {
             uint32_t r[32];
             tmem_ld32(acc + 32 * h, r);
-            if (lane == 0) bulk_wait_read<1>();
+            if (lane == 0) bulk_wait_read<0>();
             tmem_wait_ld();
             __syncwarp();
-            uint8_t* const mine = slot0 + flip * kSlotBytes + lane_off;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(mine + ((j ^ sw) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+              *reinterpret_cast<uint4*>(mine + ((j ^ sw) << 4)) =
+                  make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&p.tpart, slot0_addr + flip * kSlotBytes, g * 64 + 32 * h,
-                           w.part * 256 + (int)rank * 128 + quarter * 32);
+              tma_store_2d(&p.tpart, slot, g * 64 + 32 * h, w.part * 256 + (int)rank * 128 + quarter * 32);
               bulk_commit();
             }
           }
           continue;
         }
         const int head = col / p.o_d, c = col - head * p.o_d;
-        const bool save_z = p.save_z != 0;
-        if (lane == 0) {
-          if (save_z) bulk_wait_read<0>();
-          else bulk_wait_read<1>();
-          if (p.residual) {
-            mbar_arrive_expect_tx(&sh.residual[ew], kSlotBytes);
-            tma_load_4d<1>(slot0_addr + flip * kSlotBytes, &p.tres, smem_u32(&sh.residual[ew]), c, row, head, w.batch);
-          }
-        }
-        __syncwarp();
-        uint8_t* const mine = slot0 + flip * kSlotBytes + lane_off;
-        uint8_t* const mine_z = slot0 + (flip ^ 1) * kSlotBytes + lane_off;
+        // z first, where it is saved, then the result
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          tmem_ld32(acc + 32 * h, r);
-          tmem_wait_ld();
-          if (h == 0 && p.residual) {
-            if (!__all_sync(0xffffffffu, wait(&sh.residual[ew], res_phase))) ok = false;
-            res_phase ^= 1;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
-            const int cj = col + 32 * h + 8 * j;
-            if (p.bias && cj < p.F) add_bias8(v, p.bias + cj);
-            const int off = ((4 * h + j) ^ sw) << 4;
-            if (save_z) *reinterpret_cast<uint4*>(mine_z + off) = pack8<T>(v);
-            activate_n(v, p.act);
-            if (p.residual) {
-              float x[8];
-              unpack8<T>(*reinterpret_cast<const uint4*>(mine + off), x);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] += x[i];
+        for (int pass = p.save_z ? 0 : 1; pass < 2; ++pass) {
+          const bool res = pass && p.residual;
+          const int act = pass ? p.act : kActNone;
+          if (lane == 0) {
+            bulk_wait_read<0>();
+            if (res) {
+              mbar_arrive_expect_tx(&sh.residual[ew], kSlotBytes);
+              tma_load_4d<1>(slot, &p.tres, smem_u32(&sh.residual[ew]), c, row, head, w.batch);
             }
-            *reinterpret_cast<uint4*>(mine + off) = pack8<T>(v);
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld32(acc + 32 * h, r);
+            tmem_wait_ld();
+            if (h == 0 && res) {
+              ok = wait.warp(&sh.residual[ew], res_phase) && ok;
+              res_phase ^= 1;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
+              const int cj = col + 32 * h + 8 * j;
+              if (p.bias && cj < p.F) add_bias8(v, p.bias + cj);
+              uint4* const at = reinterpret_cast<uint4*>(mine + (((4 * h + j) ^ sw) << 4));
+              activate_n(v, act);
+              if (res) {
+                float x[8];
+                unpack8<T>(*at, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += x[i];
+              }
+              *at = pack8<T>(v);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(pass ? &p.tout : &p.tz, slot, c, row, head, w.batch);
+            bulk_commit();
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_4d(&p.tout, slot0_addr + flip * kSlotBytes, c, row, head, w.batch);
-          if (save_z) tma_store_4d(&p.tz, slot0_addr + (flip ^ 1) * kSlotBytes, c, row, head, w.batch);
-          bulk_commit();
-        }
-        flip ^= 1;
       }
       tc_fence_before();
       __syncwarp();

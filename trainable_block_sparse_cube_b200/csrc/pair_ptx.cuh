@@ -8,6 +8,17 @@
 namespace vsa {
 namespace ptx {
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 // Tiled 4-D load global -> this CTA's shared memory, completing on an mbarrier
 // (transaction bytes). CG = 2: the barrier, a shared::cluster address, may be
