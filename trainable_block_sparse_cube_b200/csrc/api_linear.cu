@@ -159,17 +159,11 @@ vsa_status encode(CUtensorMap* m, const RowsView& v, long long rows, long long b
              : VSA_ERR_CUDA;
 }
 
-// The parts of split tiles: `rows` rows of bn fp32, written in boxes of 32 x 32.
-vsa_status encode_parts(CUtensorMap* m, void* data, long long rows, int bn) {
-  vsa::EncodeTiledFn enc = vsa::get_encode_fn();
-  if (!enc) return VSA_ERR_CUDA;
-  const cuuint64_t dims[2] = {(cuuint64_t)bn, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)bn * 4};
-  const cuuint32_t box[2] = {32, 32}, one[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-                 CUDA_SUCCESS
-             ? VSA_OK
-             : VSA_ERR_CUDA;
+// Every 16 channels of a row start on a 32-byte boundary. (Strides of
+// dimensions of length 1 count too: they only cost the wider access.)
+bool aligned32(const RowsView& v) {
+  return !v.data || ((reinterpret_cast<uintptr_t>(v.data) & 31u) == 0 && v.D % 16 == 0 &&
+                     (v.s_b % 16 | v.s_h % 16 | v.s_n % 16) == 0);
 }
 
 struct Epilogue {
@@ -188,14 +182,15 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   const int half = p.t.bn / 2;
   vsa_status e = encode(&g.ta, a, run_rows, runs, weight ? 64 : 128, type);
   if (e == VSA_OK) e = encode(&g.tb, b, b_rows, weight ? runs : 1, p.kind == vsa::kGemmForward ? half : 64, type);
-  if (e == VSA_OK) e = encode(&g.tout, ep.out, p.rows, p.batches, 32, type);
-  if (e == VSA_OK && ep.residual.data) e = encode(&g.tres, ep.residual, p.rows, p.batches, 32, type);
-  if (e == VSA_OK && ep.z.data) e = encode(&g.tz, ep.z, p.rows, p.batches, 32, type);
-  if (e == VSA_OK && p.t.rest) e = encode_parts(&g.tpart, workspace, p.t.rest * p.t.splits * 256, p.t.bn);
   if (e != VSA_OK) return e;
+  g.out = ep.out;
+  g.residual = ep.residual;
+  g.z = ep.z;
+  g.partial = static_cast<float*>(workspace);
+  g.wide = aligned32(ep.out) && aligned32(ep.residual) && aligned32(ep.z) &&
+           (reinterpret_cast<uintptr_t>(workspace) & 31u) == 0;
   g.a_d = a.D;
   g.b_d = b.D;
-  g.o_d = ep.out.D;
   g.bn = p.t.bn;
   g.batches = (int)p.batches;
   g.rows = (int)p.rows;
@@ -206,8 +201,6 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   g.kblocks_batch = (int)p.kblocks_batch;
   g.bias = ep.bias;
   g.act = ep.act;
-  g.residual = ep.residual.data != nullptr;
-  g.save_z = ep.z.data != nullptr;
   g.stall = g_stall.load(std::memory_order_relaxed);
   g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   const long long units = p.t.whole + p.t.rest * p.t.splits;

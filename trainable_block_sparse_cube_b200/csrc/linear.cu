@@ -13,7 +13,7 @@
 //    (cta_group::2) reads both halves, so a CTA loads 16 + bn/16 KB a 64-long
 //    step of the contraction instead of the 16 + bn/8 KB of a lone CTA: the
 //    L2 -> SM rate, not the tensor cores, would bound the latter. One thread
-//    issues the loads (6 stages of 32 KB), one the MMAs, eight warps the
+//    issues the loads (7 stages of 32 KB), one the MMAs, eight warps the
 //    epilogue of the tile before (two accumulators of up to 256 columns fill
 //    the SM's tensor memory). Bound by the tensor cores where the product is
 //    large.
@@ -41,19 +41,17 @@ using namespace ptx;
 
 __device__ int g_linear_error;
 
-constexpr int kStages = 6, kStageBytes = 32768, kTileA = 16384;
+constexpr int kStages = 7, kStageBytes = 32768, kTileA = 16384;
 constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
-constexpr int kSlotBytes = 4096;  // 32 rows of 128 bytes
 constexpr int kAccColumns = 256;
 
 struct Barriers {
   uint64_t full[kStages], empty[kStages];
   uint64_t acc_full[2], acc_empty[2];
-  uint64_t residual[kEpiWarps];
   uint64_t drained;
   uint32_t tmem;
 };
-constexpr int kGemmSmem = 1024 + kStages * kStageBytes + kEpiWarps * kSlotBytes + (int)sizeof(Barriers);
+constexpr int kGemmSmem = 1024 + kStages * kStageBytes + (int)sizeof(Barriers);
 static_assert(kGemmSmem <= 227 * 1024, "shared memory");
 
 // ---------------------------------------------------------------- arithmetic
@@ -183,6 +181,50 @@ __device__ __forceinline__ void add_bias8(float (&v)[8], const float* bias) {
   v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
 }
 
+__device__ __forceinline__ void add_bias16(float (&v)[16], const float* bias, bool both) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= 2 && !both) break;
+    const float4 a = __ldg(reinterpret_cast<const float4*>(bias) + i);
+    v[4 * i] += a.x, v[4 * i + 1] += a.y, v[4 * i + 2] += a.z, v[4 * i + 3] += a.w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void pack16(const float (&v)[16], uint32_t (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+}
+
+// 32 bytes, in one access where `wide` says that they are aligned to it; only
+// the first 16 unless `both`.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide, bool both) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    if (both) static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8], bool wide, bool both) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0];
+    const uint4 b = both ? static_cast<const uint4*>(p)[1] : make_uint4(0, 0, 0, 0);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T* view_at(const RowsView& v, int b, int head, int n) {
+  return static_cast<T*>(v.data) + b * v.s_b + head * v.s_h + n * v.s_n;
+}
 template <typename T>
 __device__ __forceinline__ T* at(const RowsView& v, int b, int n, int c) {
   return static_cast<T*>(v.data) + b * v.s_b + (c / v.D) * v.s_h + n * v.s_n + c % v.D;
@@ -259,8 +301,7 @@ template <int KIND, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  uint8_t* const slots = raw + (base - smem_u32(raw)) + kStages * kStageBytes;
-  Barriers& sh = *reinterpret_cast<Barriers*>(slots + kEpiWarps * kSlotBytes);
+  Barriers& sh = *reinterpret_cast<Barriers*>(raw + (base - smem_u32(raw)) + kStages * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = (unsigned)p.units;
@@ -270,7 +311,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
-    for (int i = 0; i < kEpiWarps; ++i) mbar_init(&sh.residual[i], 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     prefetch_tmap(&p.ta);
@@ -327,17 +367,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], pair_bytes);
           if (load) {
             if (KIND == kGemmWeight) {
-              tma_load_4d<2>(a, &p.ta, bar, cc0, k, ch0, kh);
-              tma_load_4d<2>(b, &p.tb, bar, bc0, k, bh0, kh);
-              tma_load_4d<2>(a + 8192, &p.ta, bar, cc1, k, ch1, kh);
-              if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, bc1, k, bh1, kh);
+              tma_load_4d_pair(a, &p.ta, bar, cc0, k, ch0, kh);
+              tma_load_4d_pair(b, &p.tb, bar, bc0, k, bh0, kh);
+              tma_load_4d_pair(a + 8192, &p.ta, bar, cc1, k, ch1, kh);
+              if (b_boxes > 1) tma_load_4d_pair(b + 8192, &p.tb, bar, bc1, k, bh1, kh);
             } else {
-              tma_load_4d<2>(a, &p.ta, bar, k, row, kh, w.batch);
+              tma_load_4d_pair(a, &p.ta, bar, k, row, kh, w.batch);
               if (KIND == kGemmForward) {
-                tma_load_4d<2>(b, &p.tb, bar, kb * 64, col, 0, 0);
+                tma_load_4d_pair(b, &p.tb, bar, kb * 64, col, 0, 0);
               } else {
-                tma_load_4d<2>(b, &p.tb, bar, col, kb * 64, 0, 0);
-                if (b_boxes > 1) tma_load_4d<2>(b + 8192, &p.tb, bar, col + 64, kb * 64, 0, 0);
+                tma_load_4d_pair(b, &p.tb, bar, col, kb * 64, 0, 0);
+                if (b_boxes > 1) tma_load_4d_pair(b + 8192, &p.tb, bar, col + 64, kb * 64, 0, 0);
               }
             }
           }
@@ -390,93 +430,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       }
     }
   } else {
-    // ---- epilogue: a warp takes 32 rows and every second 64-column group of the
-    // tile, through a slot of 32 swizzled 128-byte rows
-    const int ew = warp - 2, quarter = warp & 3;
-    uint8_t* const mine = slots + ew * kSlotBytes + lane * 128;
-    const uint32_t slot = smem_u32(slots + ew * kSlotBytes);
-    const int sw = lane & 7;
+    // ---- epilogue: a warp takes 32 rows, a row a lane, and every second
+    // 64-column group of the tile, from tensor memory straight to global memory
+    // in whole 32-byte sectors. Shared memory has no bandwidth to spare: the
+    // MMAs read 64 bytes a cycle of it and the loads write as many (%STG%).
+    const int quarter = warp & 3;
     int tile = 0;
-    uint32_t res_phase = 0;
-    bool ok = true;
-    for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
+    for (unsigned u = pair; u < units; u += pairs, ++tile) {
       const Unit w(p, u);
       const int buf = tile & 1;
       if (!wait.warp(&sh.acc_full[buf], (tile >> 1) & 1)) break;
       tc_fence_after();
-      const int row = w.row0 + (int)rank * 128 + quarter * 32;
-      for (int g = ew >> 2; g * 64 < p.bn; g += 2) {
+      const int in_tile = (int)rank * 128 + quarter * 32 + lane, n = w.row0 + in_tile;
+      const bool live = n < p.rows;
+      for (int g = (warp - 2) >> 2; g * 64 < p.bn; g += 2) {
         const int col = w.col0 + g * 64;
-        const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 64);
-        if (row >= p.rows || col >= p.F) break;
-        if (w.part >= 0) {
-          // a part of the contraction: fp32 sums, 32 columns a store
+        if (n - lane >= p.rows || col >= p.F) break;
+        const int head = col / p.out.D, c = col - head * p.out.D;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_ld32(acc + 32 * h, r);
-            if (lane == 0) bulk_wait_read<0>();
+        for (int h = 0; h < 2 && col + 32 * h < p.F; ++h) {
+          uint32_t r[32];
+          const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 64 + 32 * h);
+          if (w.part >= 0) {  // a part of the contraction: fp32 sums
+            tmem_ld32(acc, r);
             tmem_wait_ld();
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(mine + ((j ^ sw) << 4)) =
-                  make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&p.tpart, slot, g * 64 + 32 * h, w.part * 256 + (int)rank * 128 + quarter * 32);
-              bulk_commit();
-            }
-          }
-          continue;
-        }
-        const int head = col / p.o_d, c = col - head * p.o_d;
-        // z first, where it is saved, then the result
-#pragma unroll 1
-        for (int pass = p.save_z ? 0 : 1; pass < 2; ++pass) {
-          const bool res = pass && p.residual;
-          const int act = pass ? p.act : kActNone;
-          if (lane == 0) {
-            bulk_wait_read<0>();
-            if (res) {
-              mbar_arrive_expect_tx(&sh.residual[ew], kSlotBytes);
-              tma_load_4d<1>(slot, &p.tres, smem_u32(&sh.residual[ew]), c, row, head, w.batch);
-            }
-          }
-          __syncwarp();
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_ld32(acc + 32 * h, r);
-            tmem_wait_ld();
-            if (h == 0 && res) {
-              ok = wait.warp(&sh.residual[ew], res_phase) && ok;
-              res_phase ^= 1;
-            }
+            float* const dst = p.partial + ((long long)w.part * 256 + in_tile) * p.bn + g * 64 + 32 * h;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              float v[8];
+              uint32_t v[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * j + i]);
-              const int cj = col + 32 * h + 8 * j;
-              if (p.bias && cj < p.F) add_bias8(v, p.bias + cj);
-              uint4* const at = reinterpret_cast<uint4*>(mine + (((4 * h + j) ^ sw) << 4));
-              activate_n(v, act);
-              if (res) {
-                float x[8];
-                unpack8<T>(*at, x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += x[i];
-              }
-              *at = pack8<T>(v);
+              for (int i = 0; i < 8; ++i) v[i] = r[8 * j + i];
+              if (live) store32(dst + 8 * j, v, p.wide, true);
             }
+            continue;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_4d(pass ? &p.tout : &p.tz, slot, c, row, head, w.batch);
-            bulk_commit();
+          const int ch = c + 32 * h, left = p.F - (col + 32 * h);  // columns up to the edge, a multiple of 8
+          uint32_t x[2][8];
+          if (p.residual.data) {
+            const T* const src = view_at<T>(p.residual, w.batch, head, n) + ch;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (live && 16 * j < left) load32(src + 16 * j, x[j], p.wide, left > 16 * j + 8);
+          }
+          tmem_ld32(acc, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (16 * j >= left) break;
+            const bool both = left > 16 * j + 8;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
+            if (p.bias) add_bias16(v, p.bias + col + 32 * h + 16 * j, both);
+            uint32_t o[8];
+            if (p.z.data) {
+              pack16<T>(v, o);
+              if (live) store32(view_at<T>(p.z, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
+            }
+            activate_n(v, p.act);
+            if (p.residual.data) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 f = unpack2<T>(x[j][i]);
+                v[2 * i] += f.x;
+                v[2 * i + 1] += f.y;
+              }
+            }
+            pack16<T>(v, o);
+            if (live) store32(view_at<T>(p.out, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
           }
         }
       }
@@ -484,7 +505,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sh.acc_empty[buf]), 0));
     }
-    if (lane == 0) bulk_wait0();
   }
   __syncwarp();
   tc_fence_before();

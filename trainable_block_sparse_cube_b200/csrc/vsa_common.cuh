@@ -199,14 +199,15 @@ struct RowsView {
   long long s_b, s_h, s_n;
 };
 
-// out = A B^T on the tensor cores. A, out, the residual and z are 4-D maps
-// (channel of a head, row, head, batch), B of the weights (column, row, 1, 1),
-// in 128-byte swizzle with boxes of 64 channels. A K-major operand is read along
+// out = A B^T on the tensor cores. A and B are 4-D maps (channel of a head,
+// row, head, batch) in 128-byte swizzle with boxes of 64 channels. A K-major operand is read along
 // its channels, an MN-major one along its rows.
 struct GemmParams {
-  CUtensorMap ta, tb, tout, tres, tz;
-  CUtensorMap tpart;        // fp32 parts of split tiles: rows (part, row of the tile) of bn, 32 x 32 boxes
-  int a_d, b_d, o_d;        // channels of a head of A, B, out
+  CUtensorMap ta, tb;
+  RowsView out, residual, z;  // residual, z: data null for none
+  float* partial;           // parts of split tiles [splits, rest, 256, bn]
+  int wide;                 // out, residual, z and partial are accessed in aligned 32-byte pieces
+  int a_d, b_d;             // channels of a head of A, B
   int bn;                   // columns of a tile: 128, 192 or 256
   int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
   int rows;                 // rows of a batch
@@ -215,7 +216,7 @@ struct GemmParams {
   int kblocks_batch;        // kGemmWeight: blocks of a batch of rows
   int whole, rest, splits;  // tiles computed in one go, and those computed in parts of the contraction
   const float* bias;        // [F] or null
-  int act, residual, save_z;
+  int act;
   int stall;                // test hook: no operand is loaded
   unsigned long long wait_ns;
   long long units;          // whole + rest x splits
