@@ -97,7 +97,19 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // accuracy where z is far below 0.
 constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.07135481282805f;  // 2 sqrt(2/pi), that times 0.044715
 
-__device__ __forceinline__ float sigmoid_times(float z, float v) { return __fdividef(z, 1.f + __expf(-v)); }
+// The hardware's 2^x and 1/x; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid(float v) { return rcp_approx(1.f + exp2_approx(-kLog2e * v)); }
 
 // gelu is z P(z) with the normal distribution function P. Its tail
 // h = P(-|z|) = exp(-z^2 / 2) t q(t) with t = 1 / (1 + 0.3111 |z|): q is of
@@ -105,8 +117,8 @@ __device__ __forceinline__ float sigmoid_times(float z, float v) { return __fdiv
 // (1.9e-7; 4.7e-7 as evaluated), so h keeps its accuracy far below 0, at a
 // quarter of the instructions of erfcf (16384 x 1536 x 6144: 341 -> %GELU% us).
 __device__ __forceinline__ float normal_tail(float a, float* density) {
-  const float t = __fdividef(1.f, fmaf(0.3111269772052765f, a, 1.f));
-  const float e = __expf(-0.5f * a * a);
+  const float t = rcp_approx(fmaf(0.3111269772052765f, a, 1.f));
+  const float e = exp2_approx(-0.5f * kLog2e * (a * a));
   float q = 0.03574991226196289f;
   q = fmaf(q, t, -0.13957644999027252f);
   q = fmaf(q, t, 0.14943377673625946f);
@@ -121,8 +133,8 @@ __device__ __forceinline__ float normal_tail(float a, float* density) {
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-  if (ACT == kActSilu) return sigmoid_times(z, z);
-  if (ACT == kActGeluTanh) return sigmoid_times(z, z * fmaf(kTanhB, z * z, kTanhA));
+  if (ACT == kActSilu) return z * sigmoid(z);
+  if (ACT == kActGeluTanh) return z * sigmoid(z * fmaf(kTanhB, z * z, kTanhA));
   if (ACT == kActGelu) {
     float e;
     const float a = fminf(fabsf(z), 20.f);  // the tail is 0 beyond: an infinite z meets no 0 x infinity
@@ -134,11 +146,11 @@ __device__ __forceinline__ float activate(float z) {
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
   if (ACT == kActSilu) {
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
+    const float s = sigmoid(z);
     return fmaf(z * s, 1.f - s, s);
   }
   if (ACT == kActGeluTanh) {
-    const float s = __fdividef(1.f, 1.f + __expf(-z * fmaf(kTanhB, z * z, kTanhA)));
+    const float s = sigmoid(z * fmaf(kTanhB, z * z, kTanhA));
     return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z * z, kTanhA), s);
   }
   if (ACT == kActGelu) {  // P(z) + z exp(-z^2 / 2) / sqrt(2 pi)
