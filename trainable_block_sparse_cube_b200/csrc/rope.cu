@@ -17,10 +17,13 @@
 // Bound by HBM: a row is read once and written once (the norm's backward
 // reads x and dy). A lane moves 8 channels, a power of two of lanes a row, and
 // a thread keeps one (token, 8 channels) place for all heads of its unit, so
-// an angle is computed once for 24 or 80 rows of it. A unit is a tile of
-// tokens by a group of heads; the grid holds the blocks that fit on the GPU
-// and each strides over the units, the number of head groups being the one
-// whose longest block is shortest (plan_units).
+// an angle is computed once for 24 or 80 rows of it. Two heads at a time are
+// worked on as packed pairs of fp32 (half the instructions: the norm is near
+// the issue limit otherwise), while the loads of the next heads are in
+// flight. A unit is a tile of tokens by a group of heads of q or of k; the
+// grid holds the blocks that fit on the GPU and each strides over the units,
+// the number of groups being the one whose longest block is shortest
+// (plan_units).
 //
 // The weight gradients are summed per thread over its rows, per block through
 // shared memory, and over the blocks by a second kernel, always in the same
@@ -33,7 +36,7 @@ namespace vsa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 template <typename T>
 struct Row8;  // 8 channels as they lie in memory
@@ -103,11 +106,52 @@ __device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Sum over the L lanes of a row.
-template <int L>
-__device__ __forceinline__ float row_sum(float v) {
+// Two fp32 values in one register pair: the same channel of two heads.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 both(float v) { return pair2(v, v); }
+
+template <typename T>
+__device__ __forceinline__ void unpack_pair(const Row8<T>& a, const Row8<T>& b, F2 (&x)[8]) {
+  float u[8], v[8];
+  unpack(a, u);
+  unpack(b, v);
 #pragma unroll
-  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int i = 0; i < 8; ++i) x[i] = pair2(u[i], v[i]);
+}
+
+// Sums over the L lanes of a row, of both heads.
+template <int L>
+__device__ __forceinline__ F2 row_sum(F2 v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) {
+    const float2 f = split2(v);
+    v = add2(v, pair2(__shfl_xor_sync(0xffffffffu, f.x, o), __shfl_xor_sync(0xffffffffu, f.y, o)));
+  }
   return v;
 }
 
@@ -179,20 +223,25 @@ struct Place {
   }
 
   // The other channel of each pair (0 where a channel is not rotated, so that
-  // an infinity there meets no zero coefficient).
-  __device__ __forceinline__ void other(const Row8<T>& raw, const float (&x)[8], float (&xp)[8]) const {
+  // an infinity there meets no zero coefficient; `full`: all are rotated).
+  __device__ __forceinline__ void other(const Row8<T>& a, const Row8<T>& b, const F2 (&x)[8], bool full,
+                                        F2 (&xp)[8]) const {
     if (INTER) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xp[i] = turned >> i & 1u ? x[i ^ 1] : 0.f;
+      for (int i = 0; i < 8; ++i) xp[i] = x[i ^ 1];
     } else {
-      Row8<T> o;
+      Row8<T> u, v;
 #pragma unroll
-      for (int i = 0; i < Row8<T>::REGS; ++i) o.r[i] = __shfl_sync(0xffffffffu, raw.r[i], partner);
-      unpack(o, xp);
-      if (!turned) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xp[i] = 0.f;
+      for (int i = 0; i < Row8<T>::REGS; ++i) {
+        u.r[i] = __shfl_sync(0xffffffffu, a.r[i], partner);
+        v.r[i] = __shfl_sync(0xffffffffu, b.r[i], partner);
       }
+      unpack_pair(u, v, xp);
+    }
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!(turned >> i & 1u)) xp[i] = 0;
     }
   }
 };
@@ -226,9 +275,25 @@ __device__ __forceinline__ void stage_rotation(const RopeParams& p, double* freq
   __syncthreads();
 }
 
-// U heads' rows in flight at a time.
+// Unit u: heads lo .. hi of a tensor, batch b, tile of tokens. All units of q
+// come before those of k.
+struct Unit {
+  int t, b, tile, lo, hi;
+  __device__ __forceinline__ Unit(const RopeParams& p, long long u) {
+    t = u >= p.units_q;
+    if (t) u -= p.units_q;
+    const int groups = p.groups[t], heads = p.t[t].heads, g = (int)(u % groups);
+    const long long bt = u / groups;
+    b = (int)(bt / p.tiles);
+    tile = (int)(bt - (long long)b * p.tiles);
+    lo = (int)((long long)heads * g / groups);
+    hi = (int)((long long)heads * (g + 1) / groups);
+  }
+};
+
+// U heads' rows (an even number) are worked on while the next U are loaded.
 template <typename T, int L, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ double freq[kRopePairs];
   __shared__ int axis[kRopePairs];
   stage_rotation(p, freq, axis);
@@ -236,70 +301,71 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
   me.init(p.D, p.rot);
   constexpr int ROWS = kThreads / L;
   const float inv_d = 1.f / (float)p.D;
+  const bool full = p.rot == p.D;
   for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
-    const int g = (int)(u % p.groups);
-    const long long bt = u / p.groups;
-    const int b = (int)(bt / p.tiles), n = (int)(bt % p.tiles) * ROWS + me.lane_row;
+    const Unit w(p, u);
+    const RopeTensor& x = p.t[w.t];
+    const int n = w.tile * ROWS + me.lane_row;
     const bool live = n < p.N && me.in_row;
-    double pos[kRopeAxes];
-    token_positions(p, b, n < p.N ? n : 0, pos);
-    me.angles(freq, axis, pos, p.rot, p.back != 0);
-    const int total = p.t[0].heads + p.t[1].heads;
-    const int h_lo = (int)((long long)total * g / p.groups), h_hi = (int)((long long)total * (g + 1) / p.groups);
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-      const RopeTensor& x = p.t[t];
-      const int first = t ? p.t[0].heads : 0;
-      const int lo = max(h_lo - first, 0), hi = min(h_hi - first, x.heads);
-      if (lo >= hi) continue;
-      // y_i = r (x_i A_i + x'_i B_i), the weight folded into A and B
-      float A[8], B[8];
+    const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + w.lo * x.in_h + me.chunk * 8;
+    T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + w.lo * x.out_h + me.chunk * 8;
+    const int heads = w.hi - w.lo;
+    Row8<T> next[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) A[i] = me.c[i], B[i] = me.s[i];
-      if (x.w && me.in_row) {
-        const float4 w0 = reinterpret_cast<const float4*>(x.w + me.chunk * 8)[0];
-        const float4 w1 = reinterpret_cast<const float4*>(x.w + me.chunk * 8)[1];
-        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    for (int k = 0; k < U; ++k) {
+      next[k] = Row8<T>{};
+      if (live && k < heads) next[k] = load8(src + k * x.in_h);
+    }
+    double pos[kRopeAxes];
+    token_positions(p, w.b, n < p.N ? n : 0, pos);
+    me.angles(freq, axis, pos, p.rot, p.back != 0);
+    // y_i = r (x_i A_i + x'_i B_i), the weight folded into A and B
+    F2 A[8], B[8];
+    float wa[8], wb[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
+    if (x.w && me.in_row) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wa[i] = x.w[me.chunk * 8 + i];
+      const int pc = INTER ? me.chunk : me.chunk + (me.partner - (int)(threadIdx.x & 31));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wb[i] = INTER ? wa[i ^ 1] : x.w[pc * 8 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) A[i] = both(me.c[i] * wa[i]), B[i] = both(me.s[i] * wb[i]);
+#pragma unroll 1
+    for (int h0 = 0; h0 < heads; h0 += U) {
+      Row8<T> now[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        now[k] = next[k];
+        if (live && h0 + U + k < heads) next[k] = load8(src + (h0 + U + k) * x.in_h);
+      }
+#pragma unroll
+      for (int k = 0; k < U; k += 2) {
+        if (k && h0 + k >= heads) break;
+        F2 v[8], o[8];
+        unpack_pair(now[k], now[k + 1], v);
+        me.other(now[k], now[k + 1], v, full, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fma2(o[i], B[i], mul2(v[i], A[i]));
+        if (p.norm) {
+          F2 ss = mul2(v[0], v[0]);
+#pragma unroll
+          for (int i = 1; i < 8; ++i) ss = fma2(v[i], v[i], ss);
+          const float2 m = split2(fma2(row_sum<L>(ss), both(inv_d), both(p.eps)));
+          const F2 r = pair2(rsqrtf(m.x), rsqrtf(m.y));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = mul2(o[i], r);
+        }
+        float a[8], b[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          A[i] *= w[i];
-          if (INTER) B[i] *= w[i ^ 1];
+          const float2 f = split2(o[i]);
+          a[i] = f.x, b[i] = f.y;
         }
-        if (!INTER && me.turned) {
-          const int pc = me.chunk + (me.partner - (int)(threadIdx.x & 31));
-          const float4 v0 = reinterpret_cast<const float4*>(x.w + pc * 8)[0];
-          const float4 v1 = reinterpret_cast<const float4*>(x.w + pc * 8)[1];
-          const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) B[i] *= v[i];
-        }
-      }
-      const T* src = static_cast<const T*>(x.in) + b * x.in_b + n * x.in_n + me.chunk * 8;
-      T* dst = static_cast<T*>(x.out) + b * x.out_b + n * x.out_n + me.chunk * 8;
-#pragma unroll 1
-      for (int h0 = lo; h0 < hi; h0 += U) {
-        Row8<T> raw[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          raw[k] = Row8<T>{};
-          if (live && h0 + k < hi) raw[k] = load8(src + (h0 + k) * x.in_h);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          float v[8], o[8];
-          unpack(raw[k], v);
-          me.other(raw[k], v, o);
-          float r = 1.f;
-          if (p.norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-            r = rsqrtf(fmaf(row_sum<L>(ss), inv_d, p.eps));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = r * fmaf(o[i], B[i], v[i] * A[i]);
-          if (live && h0 + k < hi) store8(dst + (h0 + k) * x.out_h, v);
-        }
+        if (live) store8(dst + (h0 + k) * x.out_h, a);
+        if (live && h0 + k + 1 < heads) store8(dst + (h0 + k + 1) * x.out_h, b);
       }
     }
   }
@@ -307,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
 
 // Backward of the norm with the rotation: x.in = x, x.dy = dy, x.out = dx, the
 // block's weight gradients to p.partial[block][tensor][D].
-template <typename T, int L, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
+template <typename T, int L, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
   __shared__ double freq[kRopePairs];
   __shared__ int axis[kRopePairs];
   __shared__ float part[kThreads * 8];
@@ -317,83 +383,99 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_backward_kernel(const _
   me.init(p.D, p.rot);
   constexpr int ROWS = kThreads / L;
   const float inv_d = 1.f / (float)p.D;
-  float acc[2][8];
+  const bool full = p.rot == p.D;
+  F2 acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
-  for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
-    const int g = (int)(u % p.groups);
-    const long long bt = u / p.groups;
-    const int b = (int)(bt / p.tiles), n = (int)(bt % p.tiles) * ROWS + me.lane_row;
-    const bool live = n < p.N && me.in_row;
-    double pos[kRopeAxes];
-    token_positions(p, b, n < p.N ? n : 0, pos);
-    me.angles(freq, axis, pos, p.rot, true);
-    const int total = p.t[0].heads + p.t[1].heads;
-    const int h_lo = (int)((long long)total * g / p.groups), h_hi = (int)((long long)total * (g + 1) / p.groups);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const RopeTensor& x = p.t[t];
-      const int first = t ? p.t[0].heads : 0;
-      const int lo = max(h_lo - first, 0), hi = min(h_hi - first, x.heads);
-      if (lo >= hi) continue;
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = x.w && me.in_row ? x.w[me.chunk * 8 + i] : 1.f;
-      const T* src = static_cast<const T*>(x.in) + b * x.in_b + n * x.in_n + me.chunk * 8;
-      const T* dsrc = static_cast<const T*>(x.dy) + b * x.dy_b + n * x.dy_n + me.chunk * 8;
-      T* dst = static_cast<T*>(x.out) + b * x.out_b + n * x.out_n + me.chunk * 8;
-#pragma unroll 1
-      for (int h0 = lo; h0 < hi; h0 += U) {
-        Row8<T> rx[U], rd[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          rx[k] = rd[k] = Row8<T>{};
-          if (live && h0 + k < hi) {
-            rx[k] = load8(src + (h0 + k) * x.in_h);
-            rd[k] = load8(dsrc + (h0 + k) * x.dy_h);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          float v[8], d[8], o[8];
-          unpack(rd[k], d);
-          me.other(rd[k], d, o);
-          unpack(rx[k], v);
-          float ss = 0.f, sg = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            d[i] = fmaf(o[i], me.s[i], d[i] * me.c[i]);  // g
-            ss = fmaf(v[i], v[i], ss);
-            sg = fmaf(d[i] * w[i], v[i], sg);
-          }
-          ss = row_sum<L>(ss);
-          sg = row_sum<L>(sg);
-          const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-          const float q = r * r * (sg * inv_d);
-          // A row outside the tensor adds nothing: its x is 0, but its r may be infinite (eps = 0).
-          const bool row = live && h0 + k < hi;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (row) acc[t][i] = fmaf(d[i], v[i] * r, acc[t][i]);
-            v[i] = r * fmaf(-v[i], q, d[i] * w[i]);
-          }
-          if (row) store8(dst + (h0 + k) * x.out_h, v);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int i = 0; i < 8; ++i) acc[i] = 0;
+  int now_t = 0;
+  // Sums the threads' acc over the tile's rows into the block's partial row.
+  auto flush = [&](int t) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[(me.lane_row * L + me.chunk) * 8 + i] = acc[t][i];
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = split2(acc[i]);
+      part[(me.lane_row * L + me.chunk) * 8 + i] = f.x + f.y;
+      acc[i] = 0;
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < p.D; d += kThreads) {
       float s = 0.f;
       for (int r = 0; r < ROWS; ++r) s += part[r * L * 8 + d];
       p.partial[((size_t)blockIdx.x * 2 + t) * p.D + d] = s;
     }
+  };
+  for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
+    const Unit w(p, u);
+    if (w.t != now_t) flush(0), now_t = 1;
+    const RopeTensor& x = p.t[w.t];
+    const int n = w.tile * ROWS + me.lane_row;
+    const bool live = n < p.N && me.in_row;
+    const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + w.lo * x.in_h + me.chunk * 8;
+    const T* dsrc = static_cast<const T*>(x.dy) + w.b * x.dy_b + n * x.dy_n + w.lo * x.dy_h + me.chunk * 8;
+    T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + w.lo * x.out_h + me.chunk * 8;
+    const int heads = w.hi - w.lo;
+    Row8<T> nx[2], nd[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      nx[k] = nd[k] = Row8<T>{};
+      if (live && k < heads) nx[k] = load8(src + k * x.in_h), nd[k] = load8(dsrc + k * x.dy_h);
+    }
+    double pos[kRopeAxes];
+    token_positions(p, w.b, n < p.N ? n : 0, pos);
+    me.angles(freq, axis, pos, p.rot, true);
+    float wt[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wt[i] = x.w && me.in_row ? x.w[me.chunk * 8 + i] : 1.f;
+#pragma unroll 1
+    for (int h0 = 0; h0 < heads; h0 += 2) {
+      F2 v[8], g[8], gw[8];
+      const bool second = h0 + 1 < heads;
+      {
+        F2 d[8], o[8];
+        unpack_pair(nd[0], nd[1], d);
+        me.other(nd[0], nd[1], d, full, o);
+        unpack_pair(nx[0], nx[1], v);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          nx[k] = nd[k] = Row8<T>{};
+          if (live && h0 + 2 + k < heads) {
+            nx[k] = load8(src + (h0 + 2 + k) * x.in_h);
+            nd[k] = load8(dsrc + (h0 + 2 + k) * x.dy_h);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = fma2(o[i], both(me.s[i]), mul2(d[i], both(me.c[i])));
+      }
+      F2 ss = 0, sg = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        gw[i] = mul2(g[i], both(wt[i]));
+        ss = fma2(v[i], v[i], ss);
+        sg = fma2(gw[i], v[i], sg);
+      }
+      const float2 m = split2(fma2(row_sum<L>(ss), both(inv_d), both(p.eps)));
+      // A row outside the tensor adds nothing: its x is 0, but its r may be infinite (eps = 0).
+      const F2 r = pair2(live ? rsqrtf(m.x) : 0.f, live && second ? rsqrtf(m.y) : 0.f);
+      const F2 q = mul2(mul2(r, row_sum<L>(sg)), both(-inv_d));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = mul2(v[i], r);
+        acc[i] = fma2(g[i], v[i], acc[i]);
+        v[i] = fma2(v[i], mul2(q, r), mul2(gw[i], r));
+      }
+      float a[8], b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = split2(v[i]);
+        a[i] = f.x, b[i] = f.y;
+      }
+      if (live) store8(dst + h0 * x.out_h, a);
+      if (live && second) store8(dst + (h0 + 1) * x.out_h, b);
+    }
   }
+  // A tensor without a unit in this block has zeros.
+  flush(now_t);
+  if (!now_t) flush(1);
 }
 
 // Sums the blocks' weight gradients: 32 channels of one tensor a block.
@@ -417,28 +499,31 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
 
 int lanes_for(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// Tiles, head groups and grid. A unit costs its heads' rows plus about three
-// rows' worth of angles; of all group counts the one whose longest block is
-// shortest is taken.
-int plan_units(RopeParams& p, int num_sms, int per_sm) {
-  const int rows = kThreads / lanes_for(p.D), heads = p.t[0].heads + p.t[1].heads;
+// Tiles, head groups and grid. A unit costs its heads' rows plus `angles` rows'
+// worth of work for its angles; of all group sizes the one whose longest block
+// is shortest is taken.
+int plan_units(RopeParams& p, int num_sms, int per_sm, int angles) {
+  const int rows = kThreads / lanes_for(p.D);
   p.tiles = (p.N + rows - 1) / rows;
   const long long tiles = (long long)p.tiles * p.B, slots = (long long)num_sms * per_sm;
+  const int most = p.t[0].heads > p.t[1].heads ? p.t[0].heads : p.t[1].heads;
   long long best = -1;
-  p.groups = 1;
-  for (int g = 1; g <= heads; ++g) {
-    const long long rounds = (tiles * g + slots - 1) / slots;
-    const long long cost = rounds * (3 + (heads + g - 1) / g);
-    if (best < 0 || cost < best) best = cost, p.groups = g;
+  int size = 1;
+  for (int n = 1; n <= most; ++n) {
+    const long long units = tiles * ((p.t[0].heads + n - 1) / n + (p.t[1].heads + n - 1) / n);
+    const long long cost = (units + slots - 1) / slots * (angles + n);
+    if (best < 0 || cost < best) best = cost, size = n;
   }
-  p.units = tiles * p.groups;
+  for (int t = 0; t < 2; ++t) p.groups[t] = (p.t[t].heads + size - 1) / size;
+  p.units_q = tiles * p.groups[0];
+  p.units = p.units_q + tiles * p.groups[1];
   return (int)(p.units < slots ? p.units : slots);
 }
 
 template <typename T, int L, bool INTER>
 cudaError_t launch_typed(const RopeParams& p, bool backward, int grid, cudaStream_t st) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;
-  if (backward) norm_rope_backward_kernel<T, L, INTER, U / 2><<<grid, kThreads, 0, st>>>(p);
+  if (backward) norm_rope_backward_kernel<T, L, INTER><<<grid, kThreads, 0, st>>>(p);
   else rope_kernel<T, L, INTER, U><<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
@@ -463,19 +548,20 @@ cudaError_t launch_any(const RopeParams& p, int type, bool backward, int grid, c
   return launch_lanes<float>(p, backward, grid, st);
 }
 
-constexpr int kForwardPerSm = 3, kBackwardPerSm = 2;
+constexpr int kForwardPerSm = 4, kBackwardPerSm = 3;
+constexpr int kForwardAngles = 5, kBackwardAngles = 3;
 
 }  // namespace
 
 cudaError_t launch_rope(RopeParams p, int type, int num_sms, cudaStream_t st) {
-  const int grid = plan_units(p, num_sms, kForwardPerSm);
+  const int grid = plan_units(p, num_sms, kForwardPerSm, kForwardAngles);
   return launch_any(p, type, false, grid, st);
 }
 
 size_t norm_rope_partial_bytes(int D, int num_sms) { return (size_t)num_sms * kBackwardPerSm * 2 * D * sizeof(float); }
 
 cudaError_t launch_norm_rope_backward(RopeParams p, int type, float* dwq, float* dwk, int num_sms, cudaStream_t st) {
-  const int grid = plan_units(p, num_sms, kBackwardPerSm);
+  const int grid = plan_units(p, num_sms, kBackwardPerSm, kBackwardAngles);
   cudaError_t e = launch_any(p, type, true, grid, st);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
   norm_weight_grad_kernel<<<dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, st>>>(p.partial, grid, p.D, dwq, dwk);
