@@ -20,9 +20,9 @@
 // an angle is computed once for 24 or 80 rows of it. Two heads at a time are
 // worked on as packed pairs of fp32 (half the instructions: the norm is near
 // the issue limit otherwise), while the loads of the next heads are in
-// flight. A unit is a tile of tokens by a group of heads of q or of k; the
-// grid holds the blocks that fit on the GPU and each strides over the units,
-// the number of groups being the one whose longest block is shortest
+// flight. A unit is a tile of tokens by a group of heads; the grid
+// holds the blocks that fit on the GPU and each strides over the units, the
+// number of groups being the one whose longest block is shortest
 // (plan_units).
 //
 // The weight gradients are summed per thread over its rows, per block through
@@ -144,15 +144,21 @@ __device__ __forceinline__ void unpack_pair(const Row8<T>& a, const Row8<T>& b, 
   for (int i = 0; i < 8; ++i) x[i] = pair2(u[i], v[i]);
 }
 
-// Sums over the L lanes of a row, of both heads.
-template <int L>
-__device__ __forceinline__ F2 row_sum(F2 v) {
+// Sums over the L lanes of a row, of both heads and N values at once (their
+// chains of shuffles run beside one another).
+template <int L, int N>
+__device__ __forceinline__ void row_sums(F2 (&v)[N]) {
 #pragma unroll
   for (int o = L / 2; o; o >>= 1) {
-    const float2 f = split2(v);
-    v = add2(v, pair2(__shfl_xor_sync(0xffffffffu, f.x, o), __shfl_xor_sync(0xffffffffu, f.y, o)));
+    F2 w[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float2 f = split2(v[k]);
+      w[k] = pair2(__shfl_xor_sync(0xffffffffu, f.x, o), __shfl_xor_sync(0xffffffffu, f.y, o));
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = add2(v[k], w[k]);
   }
-  return v;
 }
 
 // One thread's place in a tile and its rotation coefficients.
@@ -275,19 +281,20 @@ __device__ __forceinline__ void stage_rotation(const RopeParams& p, double* freq
   __syncthreads();
 }
 
-// Unit u: heads lo .. hi of a tensor, batch b, tile of tokens. All units of q
-// come before those of k.
+// Unit u: heads lo .. hi (those of q, then those of k), batch b, tile of tokens.
 struct Unit {
-  int t, b, tile, lo, hi;
-  __device__ __forceinline__ Unit(const RopeParams& p, long long u) {
-    t = u >= p.units_q;
-    if (t) u -= p.units_q;
-    const int groups = p.groups[t], heads = p.t[t].heads, g = (int)(u % groups);
-    const long long bt = u / groups;
+  int b, tile, lo, hi;
+  __device__ __forceinline__ Unit(const RopeParams& p, unsigned u) {
+    const unsigned g = u % p.groups, bt = u / p.groups, heads = p.t[0].heads + p.t[1].heads;
     b = (int)(bt / p.tiles);
-    tile = (int)(bt - (long long)b * p.tiles);
-    lo = (int)((long long)heads * g / groups);
-    hi = (int)((long long)heads * (g + 1) / groups);
+    tile = (int)(bt - (unsigned)b * p.tiles);
+    lo = (int)(heads * g / p.groups);
+    hi = (int)(heads * (g + 1) / p.groups);
+  }
+  // Its heads of tensor t.
+  __device__ __forceinline__ int first(const RopeParams& p, int t) const { return max(lo - (t ? p.t[0].heads : 0), 0); }
+  __device__ __forceinline__ int last(const RopeParams& p, int t) const {
+    return min(hi - (t ? p.t[0].heads : 0), p.t[t].heads);
   }
 };
 
@@ -302,70 +309,77 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
   constexpr int ROWS = kThreads / L;
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
-  for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
+  for (unsigned u = blockIdx.x; u < p.units; u += gridDim.x) {
     const Unit w(p, u);
-    const RopeTensor& x = p.t[w.t];
     const int n = w.tile * ROWS + me.lane_row;
     const bool live = n < p.N && me.in_row;
-    const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + w.lo * x.in_h + me.chunk * 8;
-    T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + w.lo * x.out_h + me.chunk * 8;
-    const int heads = w.hi - w.lo;
-    Row8<T> next[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      next[k] = Row8<T>{};
-      if (live && k < heads) next[k] = load8(src + k * x.in_h);
-    }
     double pos[kRopeAxes];
     token_positions(p, w.b, n < p.N ? n : 0, pos);
     me.angles(freq, axis, pos, p.rot, p.back != 0);
-    // y_i = r (x_i A_i + x'_i B_i), the weight folded into A and B
-    F2 A[8], B[8];
-    float wa[8], wb[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
-    if (x.w && me.in_row) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wa[i] = x.w[me.chunk * 8 + i];
-      const int pc = INTER ? me.chunk : me.chunk + (me.partner - (int)(threadIdx.x & 31));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wb[i] = INTER ? wa[i ^ 1] : x.w[pc * 8 + i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) A[i] = both(me.c[i] * wa[i]), B[i] = both(me.s[i] * wb[i]);
 #pragma unroll 1
-    for (int h0 = 0; h0 < heads; h0 += U) {
-      Row8<T> now[U];
+    for (int t = 0; t < 2; ++t) {
+      const RopeTensor& x = p.t[t];
+      const int lo = w.first(p, t), heads = w.last(p, t) - lo;
+      if (heads <= 0) continue;
+      const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + lo * x.in_h + me.chunk * 8;
+      T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + lo * x.out_h + me.chunk * 8;
+      Row8<T> next[U];
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        now[k] = next[k];
-        if (live && h0 + U + k < heads) next[k] = load8(src + (h0 + U + k) * x.in_h);
+        next[k] = Row8<T>{};
+        if (live && k < heads) next[k] = load8(src + k * x.in_h);
       }
+      // y_i = r (x_i A_i + x'_i B_i), the weight folded into A and B
+      F2 A[8], B[8];
 #pragma unroll
-      for (int k = 0; k < U; k += 2) {
-        if (k && h0 + k >= heads) break;
-        F2 v[8], o[8];
-        unpack_pair(now[k], now[k + 1], v);
-        me.other(now[k], now[k + 1], v, full, o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fma2(o[i], B[i], mul2(v[i], A[i]));
-        if (p.norm) {
-          F2 ss = mul2(v[0], v[0]);
-#pragma unroll
-          for (int i = 1; i < 8; ++i) ss = fma2(v[i], v[i], ss);
-          const float2 m = split2(fma2(row_sum<L>(ss), both(inv_d), both(p.eps)));
-          const F2 r = pair2(rsqrtf(m.x), rsqrtf(m.y));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = mul2(o[i], r);
-        }
-        float a[8], b[8];
+      for (int i = 0; i < 8; ++i) A[i] = both(me.c[i]), B[i] = both(me.s[i]);
+      if (x.w && me.in_row) {
+        const int pc = INTER ? me.chunk : me.chunk + (me.partner - (int)(threadIdx.x & 31));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 f = split2(o[i]);
-          a[i] = f.x, b[i] = f.y;
+          A[i] = both(me.c[i] * x.w[me.chunk * 8 + i]);
+          B[i] = both(me.s[i] * x.w[pc * 8 + (INTER ? i ^ 1 : i)]);
         }
-        if (live) store8(dst + (h0 + k) * x.out_h, a);
-        if (live && h0 + k + 1 < heads) store8(dst + (h0 + k + 1) * x.out_h, b);
+      }
+#pragma unroll 1
+      for (int h0 = 0; h0 < heads; h0 += U) {
+        Row8<T> now[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          now[k] = next[k];
+          if (live && h0 + U + k < heads) next[k] = load8(src + (h0 + U + k) * x.in_h);
+        }
+        F2 o[U / 2][8], r[U / 2];
+#pragma unroll
+        for (int k = 0; k < U / 2; ++k) {
+          F2 v[8];
+          unpack_pair(now[2 * k], now[2 * k + 1], v);
+          me.other(now[2 * k], now[2 * k + 1], v, full, o[k]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[k][i] = fma2(o[k][i], B[i], mul2(v[i], A[i]));
+          if (p.norm) {
+            r[k] = mul2(v[0], v[0]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) r[k] = fma2(v[i], v[i], r[k]);
+          }
+        }
+        if (p.norm) {
+          row_sums<L>(r);
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            const float2 m = split2(fma2(r[k], both(inv_d), both(p.eps)));
+            r[k] = pair2(rsqrtf(m.x), rsqrtf(m.y));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[k][i] = mul2(o[k][i], r[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          float a[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = k & 1 ? split2(o[k / 2][i]).y : split2(o[k / 2][i]).x;
+          if (live && h0 + k < heads) store8(dst + (h0 + k) * x.out_h, a);
+        }
       }
     }
   }
@@ -377,105 +391,103 @@ template <typename T, int L, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
   __shared__ double freq[kRopePairs];
   __shared__ int axis[kRopePairs];
-  __shared__ float part[kThreads * 8];
+  __shared__ float part[2][8][kThreads];  // a thread's sums of 8 channels over its rows so far
   stage_rotation(p, freq, axis);
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
   constexpr int ROWS = kThreads / L;
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
-  F2 acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0;
-  int now_t = 0;
-  // Sums the threads' acc over the tile's rows into the block's partial row.
-  auto flush = [&](int t) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = split2(acc[i]);
-      part[(me.lane_row * L + me.chunk) * 8 + i] = f.x + f.y;
-      acc[i] = 0;
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < p.D; d += kThreads) {
-      float s = 0.f;
-      for (int r = 0; r < ROWS; ++r) s += part[r * L * 8 + d];
-      p.partial[((size_t)blockIdx.x * 2 + t) * p.D + d] = s;
-    }
-  };
-  for (long long u = blockIdx.x; u < p.units; u += gridDim.x) {
+  for (int i = 0; i < 8; ++i) part[0][i][threadIdx.x] = part[1][i][threadIdx.x] = 0.f;
+  for (unsigned u = blockIdx.x; u < p.units; u += gridDim.x) {
     const Unit w(p, u);
-    if (w.t != now_t) flush(0), now_t = 1;
-    const RopeTensor& x = p.t[w.t];
     const int n = w.tile * ROWS + me.lane_row;
     const bool live = n < p.N && me.in_row;
-    const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + w.lo * x.in_h + me.chunk * 8;
-    const T* dsrc = static_cast<const T*>(x.dy) + w.b * x.dy_b + n * x.dy_n + w.lo * x.dy_h + me.chunk * 8;
-    T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + w.lo * x.out_h + me.chunk * 8;
-    const int heads = w.hi - w.lo;
-    Row8<T> nx[2], nd[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      nx[k] = nd[k] = Row8<T>{};
-      if (live && k < heads) nx[k] = load8(src + k * x.in_h), nd[k] = load8(dsrc + k * x.dy_h);
-    }
     double pos[kRopeAxes];
     token_positions(p, w.b, n < p.N ? n : 0, pos);
     me.angles(freq, axis, pos, p.rot, true);
-    float wt[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wt[i] = x.w && me.in_row ? x.w[me.chunk * 8 + i] : 1.f;
 #pragma unroll 1
-    for (int h0 = 0; h0 < heads; h0 += 2) {
-      F2 v[8], g[8], gw[8];
-      const bool second = h0 + 1 < heads;
-      {
-        F2 d[8], o[8];
-        unpack_pair(nd[0], nd[1], d);
-        me.other(nd[0], nd[1], d, full, o);
-        unpack_pair(nx[0], nx[1], v);
+    for (int t = 0; t < 2; ++t) {
+      const RopeTensor& x = p.t[t];
+      const int lo = w.first(p, t), heads = w.last(p, t) - lo;
+      if (heads <= 0) continue;
+      const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + lo * x.in_h + me.chunk * 8;
+      const T* dsrc = static_cast<const T*>(x.dy) + w.b * x.dy_b + n * x.dy_n + lo * x.dy_h + me.chunk * 8;
+      T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + lo * x.out_h + me.chunk * 8;
+      Row8<T> nx[2], nd[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          nx[k] = nd[k] = Row8<T>{};
-          if (live && h0 + 2 + k < heads) {
-            nx[k] = load8(src + (h0 + 2 + k) * x.in_h);
-            nd[k] = load8(dsrc + (h0 + 2 + k) * x.dy_h);
+      for (int k = 0; k < 2; ++k) {
+        nx[k] = nd[k] = Row8<T>{};
+        if (live && k < heads) nx[k] = load8(src + k * x.in_h), nd[k] = load8(dsrc + k * x.dy_h);
+      }
+      float wt[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wt[i] = x.w && me.in_row ? x.w[me.chunk * 8 + i] : 1.f;
+      F2 acc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = 0;
+#pragma unroll 1
+      for (int h0 = 0; h0 < heads; h0 += 2) {
+        F2 v[8], g[8], gw[8];
+        const bool second = h0 + 1 < heads;
+        {
+          F2 d[8], o[8];
+          unpack_pair(nd[0], nd[1], d);
+          me.other(nd[0], nd[1], d, full, o);
+          unpack_pair(nx[0], nx[1], v);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            nx[k] = nd[k] = Row8<T>{};
+            if (live && h0 + 2 + k < heads) {
+              nx[k] = load8(src + (h0 + 2 + k) * x.in_h);
+              nd[k] = load8(dsrc + (h0 + 2 + k) * x.dy_h);
+            }
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = fma2(o[i], both(me.s[i]), mul2(d[i], both(me.c[i])));
         }
+        F2 sum[2] = {0, 0};  // of x^2, of g w x
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = fma2(o[i], both(me.s[i]), mul2(d[i], both(me.c[i])));
+        for (int i = 0; i < 8; ++i) {
+          gw[i] = mul2(g[i], both(wt[i]));
+          sum[0] = fma2(v[i], v[i], sum[0]);
+          sum[1] = fma2(gw[i], v[i], sum[1]);
+        }
+        row_sums<L>(sum);
+        const float2 m = split2(fma2(sum[0], both(inv_d), both(p.eps)));
+        // A row outside the tensor adds nothing: its x is 0, but its r may be infinite (eps = 0).
+        const F2 r = pair2(live ? rsqrtf(m.x) : 0.f, live && second ? rsqrtf(m.y) : 0.f);
+        const F2 q = mul2(mul2(mul2(r, sum[1]), both(-inv_d)), r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = mul2(v[i], r);
+          acc[i] = fma2(g[i], v[i], acc[i]);
+          v[i] = fma2(v[i], q, mul2(gw[i], r));
+        }
+        float a[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = split2(v[i]);
+          a[i] = f.x, b[i] = f.y;
+        }
+        if (live) store8(dst + h0 * x.out_h, a);
+        if (live && second) store8(dst + (h0 + 1) * x.out_h, b);
       }
-      F2 ss = 0, sg = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        gw[i] = mul2(g[i], both(wt[i]));
-        ss = fma2(v[i], v[i], ss);
-        sg = fma2(gw[i], v[i], sg);
+        const float2 f = split2(acc[i]);
+        part[t][i][threadIdx.x] += f.x + f.y;
       }
-      const float2 m = split2(fma2(row_sum<L>(ss), both(inv_d), both(p.eps)));
-      // A row outside the tensor adds nothing: its x is 0, but its r may be infinite (eps = 0).
-      const F2 r = pair2(live ? rsqrtf(m.x) : 0.f, live && second ? rsqrtf(m.y) : 0.f);
-      const F2 q = mul2(mul2(r, row_sum<L>(sg)), both(-inv_d));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = mul2(v[i], r);
-        acc[i] = fma2(g[i], v[i], acc[i]);
-        v[i] = fma2(v[i], mul2(q, r), mul2(gw[i], r));
-      }
-      float a[8], b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = split2(v[i]);
-        a[i] = f.x, b[i] = f.y;
-      }
-      if (live) store8(dst + h0 * x.out_h, a);
-      if (live && second) store8(dst + (h0 + 1) * x.out_h, b);
     }
   }
-  // A tensor without a unit in this block has zeros.
-  flush(now_t);
-  if (!now_t) flush(1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < 2 * p.D; e += kThreads) {
+    const int t = e >= p.D, d = e - t * p.D;
+    float s = 0.f;
+    for (int r = 0; r < ROWS; ++r) s += part[t][d % 8][r * L + d / 8];
+    p.partial[(size_t)blockIdx.x * 2 * p.D + e] = s;
+  }
 }
 
 // Sums the blocks' weight gradients: 32 channels of one tensor a block.
@@ -500,23 +512,20 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
 int lanes_for(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
 // Tiles, head groups and grid. A unit costs its heads' rows plus `angles` rows'
-// worth of work for its angles; of all group sizes the one whose longest block
+// worth of work for its angles; of all group counts the one whose longest block
 // is shortest is taken.
 int plan_units(RopeParams& p, int num_sms, int per_sm, int angles) {
-  const int rows = kThreads / lanes_for(p.D);
+  const int rows = kThreads / lanes_for(p.D), heads = p.t[0].heads + p.t[1].heads;
   p.tiles = (p.N + rows - 1) / rows;
   const long long tiles = (long long)p.tiles * p.B, slots = (long long)num_sms * per_sm;
-  const int most = p.t[0].heads > p.t[1].heads ? p.t[0].heads : p.t[1].heads;
   long long best = -1;
-  int size = 1;
-  for (int n = 1; n <= most; ++n) {
-    const long long units = tiles * ((p.t[0].heads + n - 1) / n + (p.t[1].heads + n - 1) / n);
-    const long long cost = (units + slots - 1) / slots * (angles + n);
-    if (best < 0 || cost < best) best = cost, size = n;
+  p.groups = 1;
+  for (int g = 1; g <= heads && tiles * g < (1LL << 31); ++g) {
+    const long long rounds = (tiles * g + slots - 1) / slots;
+    const long long cost = rounds * (angles + (heads + g - 1) / g);
+    if (best < 0 || cost < best) best = cost, p.groups = g;
   }
-  for (int t = 0; t < 2; ++t) p.groups[t] = (p.t[t].heads + size - 1) / size;
-  p.units_q = tiles * p.groups[0];
-  p.units = p.units_q + tiles * p.groups[1];
+  p.units = (unsigned)(tiles * p.groups);
   return (int)(p.units < slots ? p.units : slots);
 }
 

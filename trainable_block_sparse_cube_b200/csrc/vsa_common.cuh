@@ -181,8 +181,8 @@ struct RopeParams {
   int norm;
   float eps;
   float* partial;           // norm backward: [grid, 2, D] weight gradients of the blocks
-  int tiles, groups[2];     // work split, set by the launcher
-  long long units_q, units;
+  int tiles, groups;        // work split, set by the launcher
+  unsigned units;
 };
 
 cudaError_t launch_rope(RopeParams p, int type, int num_sms, cudaStream_t st);
