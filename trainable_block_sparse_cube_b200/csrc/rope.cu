@@ -30,6 +30,7 @@
 // order: no atomics, the same bits every time.
 #include <cuda_fp16.h>
 
+#include "sm100_ptx.cuh"
 #include "vsa_common.cuh"
 
 namespace vsa {
@@ -37,6 +38,8 @@ namespace vsa {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kForwardPerSm = 4, kBackwardPerSm = 3;      // blocks of an SM
+constexpr int kForwardAngles = 5, kBackwardAngles = 3;    // rows whose work an angle's equals, see plan_units
 
 template <typename T>
 struct Row8;  // 8 channels as they lie in memory
@@ -298,15 +301,96 @@ struct Unit {
   }
 };
 
-// U heads' rows (an even number) are worked on while the next U are loaded.
+// The rows that a thread will need, in the order in which it will need them: U
+// heads a step (fewer at a tensor's end), through all its units. Each step's
+// pieces go to the thread's own slots of a stage, so no barrier is needed; a
+// stage is filled again one step after it was read.
+template <typename T, int U, bool DY, int STAGES>
+struct Feed {
+  static constexpr int PIECES = (int)sizeof(T) / 2;  // 16-byte pieces of 8 channels
+  static constexpr int SLOTS = U * (DY ? 2 : 1) * PIECES;
+  uint4 (*ring)[SLOTS][kThreads];
+  unsigned u;
+  int t, h, heads, stage_in, stage_out;
+  const T *src, *dsrc;
+  bool live, more;
+
+  __device__ __forceinline__ void start(const RopeParams& p, uint4 (*smem)[SLOTS][kThreads], int rows, int lane_row,
+                                        int chunk, bool in_row) {
+    ring = smem;
+    stage_in = stage_out = 0;
+    u = blockIdx.x;
+    t = -1;
+    h = heads = 0;
+    more = true;
+    for (int i = 0; i < STAGES - 1; ++i) load(p, rows, lane_row, chunk, in_row);
+  }
+
+  // Copies of the next step, one group (an empty one behind the last).
+  __device__ __forceinline__ void load(const RopeParams& p, int rows, int lane_row, int chunk, bool in_row) {
+    while (more && h >= heads) {  // the next tensor or unit with heads
+      if (++t == 2) t = 0, u += gridDim.x;
+      if (u >= p.units) {
+        more = false;
+        break;
+      }
+      const Unit w(p, u);
+      const RopeTensor& x = p.t[t];
+      const int lo = w.first(p, t), n = w.tile * rows + lane_row;
+      h = 0;
+      heads = w.last(p, t) - lo;
+      live = n < p.N && in_row;
+      src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + lo * x.in_h + chunk * 8;
+      if (DY) dsrc = static_cast<const T*>(x.dy) + w.b * x.dy_b + n * x.dy_n + lo * x.dy_h + chunk * 8;
+    }
+    if (more && live) {
+      const RopeTensor& x = p.t[t];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (h + k < heads) {
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            ptx::cp_async16(&ring[stage_in][k * PIECES + i][threadIdx.x], src + (h + k) * x.in_h + i * 4);
+            if (DY) ptx::cp_async16(&ring[stage_in][(U + k) * PIECES + i][threadIdx.x], dsrc + (h + k) * x.dy_h + i * 4);
+          }
+        }
+    }
+    h += U;
+    ptx::cp_async_commit();
+    if (++stage_in == STAGES) stage_in = 0;
+  }
+
+  // The oldest step's rows: zeros where there are none.
+  __device__ __forceinline__ void wait() { ptx::cp_async_wait<STAGES - 2>(); }
+  __device__ __forceinline__ Row8<T> row(int k, bool valid) const {
+    Row8<T> v{};
+    if (valid) {
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const uint4 q = ring[stage_out][k * PIECES + i][threadIdx.x];
+        v.r[4 * i] = q.x, v.r[4 * i + 1] = q.y, v.r[4 * i + 2] = q.z, v.r[4 * i + 3] = q.w;
+      }
+    }
+    return v;
+  }
+  __device__ __forceinline__ void next() {
+    if (++stage_out == STAGES) stage_out = 0;
+  }
+};
+
+// U: heads worked on at a time, an even number.
 template <typename T, int L, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int STAGES = 3;
   __shared__ double freq[kRopePairs];
   __shared__ int axis[kRopePairs];
-  stage_rotation(p, freq, axis);
+  __shared__ uint4 ring[STAGES][Feed<T, U, false, STAGES>::SLOTS][kThreads];
+  constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
-  constexpr int ROWS = kThreads / L;
+  Feed<T, U, false, STAGES> feed;
+  feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
+  stage_rotation(p, freq, axis);
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
   for (unsigned u = blockIdx.x; u < p.units; u += gridDim.x) {
@@ -321,14 +405,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
       const RopeTensor& x = p.t[t];
       const int lo = w.first(p, t), heads = w.last(p, t) - lo;
       if (heads <= 0) continue;
-      const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + lo * x.in_h + me.chunk * 8;
       T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + lo * x.out_h + me.chunk * 8;
-      Row8<T> next[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        next[k] = Row8<T>{};
-        if (live && k < heads) next[k] = load8(src + k * x.in_h);
-      }
       // y_i = r (x_i A_i + x'_i B_i), the weight folded into A and B
       F2 A[8], B[8];
 #pragma unroll
@@ -343,12 +420,12 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
       }
 #pragma unroll 1
       for (int h0 = 0; h0 < heads; h0 += U) {
+        feed.wait();
         Row8<T> now[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          now[k] = next[k];
-          if (live && h0 + U + k < heads) next[k] = load8(src + (h0 + U + k) * x.in_h);
-        }
+        for (int k = 0; k < U; ++k) now[k] = feed.row(k, live && h0 + k < heads);
+        feed.next();
+        feed.load(p, ROWS, me.lane_row, me.chunk, me.in_row);
         F2 o[U / 2][8], r[U / 2];
 #pragma unroll
         for (int k = 0; k < U / 2; ++k) {
@@ -388,14 +465,18 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
 // Backward of the norm with the rotation: x.in = x, x.dy = dy, x.out = dx, the
 // block's weight gradients to p.partial[block][tensor][D].
 template <typename T, int L, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int STAGES = sizeof(T) == 4 ? 2 : 4;
   __shared__ double freq[kRopePairs];
   __shared__ int axis[kRopePairs];
   __shared__ float part[2][8][kThreads];  // a thread's sums of 8 channels over its rows so far
-  stage_rotation(p, freq, axis);
+  __shared__ uint4 ring[STAGES][Feed<T, 2, true, STAGES>::SLOTS][kThreads];
+  constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
-  constexpr int ROWS = kThreads / L;
+  Feed<T, 2, true, STAGES> feed;
+  feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
+  stage_rotation(p, freq, axis);
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
 #pragma unroll
@@ -412,15 +493,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
       const RopeTensor& x = p.t[t];
       const int lo = w.first(p, t), heads = w.last(p, t) - lo;
       if (heads <= 0) continue;
-      const T* src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + lo * x.in_h + me.chunk * 8;
-      const T* dsrc = static_cast<const T*>(x.dy) + w.b * x.dy_b + n * x.dy_n + lo * x.dy_h + me.chunk * 8;
       T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + lo * x.out_h + me.chunk * 8;
-      Row8<T> nx[2], nd[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        nx[k] = nd[k] = Row8<T>{};
-        if (live && k < heads) nx[k] = load8(src + k * x.in_h), nd[k] = load8(dsrc + k * x.dy_h);
-      }
       float wt[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) wt[i] = x.w && me.in_row ? x.w[me.chunk * 8 + i] : 1.f;
@@ -430,20 +503,16 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
 #pragma unroll 1
       for (int h0 = 0; h0 < heads; h0 += 2) {
         F2 v[8], g[8], gw[8];
-        const bool second = h0 + 1 < heads;
+        const bool second = live && h0 + 1 < heads;
+        feed.wait();
         {
           F2 d[8], o[8];
-          unpack_pair(nd[0], nd[1], d);
-          me.other(nd[0], nd[1], d, full, o);
-          unpack_pair(nx[0], nx[1], v);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            nx[k] = nd[k] = Row8<T>{};
-            if (live && h0 + 2 + k < heads) {
-              nx[k] = load8(src + (h0 + 2 + k) * x.in_h);
-              nd[k] = load8(dsrc + (h0 + 2 + k) * x.dy_h);
-            }
-          }
+          const Row8<T> d0 = feed.row(2, live), d1 = feed.row(3, second);
+          unpack_pair(feed.row(0, live), feed.row(1, second), v);
+          feed.next();
+          feed.load(p, ROWS, me.lane_row, me.chunk, me.in_row);
+          unpack_pair(d0, d1, d);
+          me.other(d0, d1, d, full, o);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = fma2(o[i], both(me.s[i]), mul2(d[i], both(me.c[i])));
         }
@@ -457,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
         row_sums<L>(sum);
         const float2 m = split2(fma2(sum[0], both(inv_d), both(p.eps)));
         // A row outside the tensor adds nothing: its x is 0, but its r may be infinite (eps = 0).
-        const F2 r = pair2(live ? rsqrtf(m.x) : 0.f, live && second ? rsqrtf(m.y) : 0.f);
+        const F2 r = pair2(live ? rsqrtf(m.x) : 0.f, second ? rsqrtf(m.y) : 0.f);
         const F2 q = mul2(mul2(mul2(r, sum[1]), both(-inv_d)), r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -472,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_backward_kernel(const _
           a[i] = f.x, b[i] = f.y;
         }
         if (live) store8(dst + h0 * x.out_h, a);
-        if (live && second) store8(dst + (h0 + 1) * x.out_h, b);
+        if (second) store8(dst + (h0 + 1) * x.out_h, b);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -557,8 +626,6 @@ cudaError_t launch_any(const RopeParams& p, int type, bool backward, int grid, c
   return launch_lanes<float>(p, backward, grid, st);
 }
 
-constexpr int kForwardPerSm = 4, kBackwardPerSm = 3;
-constexpr int kForwardAngles = 5, kBackwardAngles = 3;
 
 }  // namespace
 
