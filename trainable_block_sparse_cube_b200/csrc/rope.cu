@@ -302,80 +302,97 @@ struct Unit {
 };
 
 // The rows that a thread will need, in the order in which it will need them: U
-// heads a step (fewer at a tensor's end), through all its units. Each step's
-// pieces go to the thread's own slots of a stage, so no barrier is needed; a
-// stage is filled again one step after it was read.
+// heads a step (zeros where there are fewer, or no such token), through all
+// its units. Each step's pieces go to the thread's own slots of a stage, so no
+// barrier is needed; a stage is filled again one step after it was read. The
+// common step is a handful of instructions: addresses are kept up by
+// additions (products and checks for every row were half of all instructions).
 template <typename T, int U, bool DY, int STAGES>
 struct Feed {
   static constexpr int PIECES = (int)sizeof(T) / 2;  // 16-byte pieces of 8 channels
   static constexpr int SLOTS = U * (DY ? 2 : 1) * PIECES;
-  uint4 (*ring)[SLOTS][kThreads];
+  static constexpr uint32_t STAGE = SLOTS * kThreads * 16, END = STAGES * STAGE;
+  uint32_t mine, in, out;  // shared address of the thread's first slot; offsets of the stages filled and read next
   unsigned u;
-  int t, h, heads, stage_in, stage_out;
+  int t, left;             // heads left in the tensor's part of the unit
   const T *src, *dsrc;
-  bool live, more;
+  long long step, dstep;   // elements between heads
+  uint32_t bytes;          // 16, or 0 for a thread outside the tensor
 
-  __device__ __forceinline__ void start(const RopeParams& p, uint4 (*smem)[SLOTS][kThreads], int rows, int lane_row,
-                                        int chunk, bool in_row) {
-    ring = smem;
-    stage_in = stage_out = 0;
+  __device__ __forceinline__ void start(const RopeParams& p, const void* smem, int rows, int lane_row, int chunk,
+                                        bool in_row) {
+    mine = ptx::smem_u32(smem) + threadIdx.x * 16;
+    in = out = 0;
     u = blockIdx.x;
     t = -1;
-    h = heads = 0;
-    more = true;
+    left = 0;
     for (int i = 0; i < STAGES - 1; ++i) load(p, rows, lane_row, chunk, in_row);
+  }
+
+  // The next tensor or unit that has heads.
+  __device__ __forceinline__ void open(const RopeParams& p, int rows, int lane_row, int chunk, bool in_row) {
+    do {
+      if (++t == 2) t = 0, u += gridDim.x;
+      if (u >= p.units) return;
+      const Unit w(p, u);
+      const RopeTensor& x = p.t[t];
+      const int lo = w.first(p, t), n = w.tile * rows + lane_row;
+      left = w.last(p, t) - lo;
+      const bool live = n < p.N && in_row;
+      bytes = live ? 16 : 0;
+      // a thread outside reads nothing, and keeps an address inside
+      const long long at = lo, b = live ? w.b : 0, m = live ? n : 0, c = live ? chunk * 8 : 0;
+      src = static_cast<const T*>(x.in) + b * x.in_b + m * x.in_n + at * x.in_h + c;
+      step = x.in_h;
+      if (DY) {
+        dsrc = static_cast<const T*>(x.dy) + b * x.dy_b + m * x.dy_n + at * x.dy_h + c;
+        dstep = x.dy_h;
+      }
+    } while (left <= 0);
+  }
+
+  __device__ __forceinline__ static void copy(uint32_t dst, const T* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   }
 
   // Copies of the next step, one group (an empty one behind the last).
   __device__ __forceinline__ void load(const RopeParams& p, int rows, int lane_row, int chunk, bool in_row) {
-    while (more && h >= heads) {  // the next tensor or unit with heads
-      if (++t == 2) t = 0, u += gridDim.x;
-      if (u >= p.units) {
-        more = false;
-        break;
-      }
-      const Unit w(p, u);
-      const RopeTensor& x = p.t[t];
-      const int lo = w.first(p, t), n = w.tile * rows + lane_row;
-      h = 0;
-      heads = w.last(p, t) - lo;
-      live = n < p.N && in_row;
-      src = static_cast<const T*>(x.in) + w.b * x.in_b + n * x.in_n + lo * x.in_h + chunk * 8;
-      if (DY) dsrc = static_cast<const T*>(x.dy) + w.b * x.dy_b + n * x.dy_n + lo * x.dy_h + chunk * 8;
-    }
-    if (more && live) {
-      const RopeTensor& x = p.t[t];
+    if (left <= 0 && u < p.units) open(p, rows, lane_row, chunk, in_row);
+    if (u < p.units) {
+      const uint32_t dst = mine + in;
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (h + k < heads) {
+      for (int k = 0; k < U; ++k) {
+        const bool there = k < left;
+        const uint32_t n = there ? bytes : 0;
 #pragma unroll
-          for (int i = 0; i < PIECES; ++i) {
-            ptx::cp_async16(&ring[stage_in][k * PIECES + i][threadIdx.x], src + (h + k) * x.in_h + i * 4);
-            if (DY) ptx::cp_async16(&ring[stage_in][(U + k) * PIECES + i][threadIdx.x], dsrc + (h + k) * x.dy_h + i * 4);
-          }
+        for (int i = 0; i < PIECES; ++i) {
+          copy(dst + (k * PIECES + i) * kThreads * 16, src + i * 4, n);
+          if (DY) copy(dst + ((U + k) * PIECES + i) * kThreads * 16, dsrc + i * 4, n);
         }
+        if (there) {
+          src += step;
+          if (DY) dsrc += dstep;
+        }
+      }
+      left -= U;
     }
-    h += U;
     ptx::cp_async_commit();
-    if (++stage_in == STAGES) stage_in = 0;
+    in = in + STAGE == END ? 0 : in + STAGE;
   }
 
-  // The oldest step's rows: zeros where there are none.
+  // The oldest step's rows have arrived.
   __device__ __forceinline__ void wait() { ptx::cp_async_wait<STAGES - 2>(); }
-  __device__ __forceinline__ Row8<T> row(int k, bool valid) const {
-    Row8<T> v{};
-    if (valid) {
+  __device__ __forceinline__ Row8<T> row(int k) const {
+    Row8<T> v;
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) {
-        const uint4 q = ring[stage_out][k * PIECES + i][threadIdx.x];
-        v.r[4 * i] = q.x, v.r[4 * i + 1] = q.y, v.r[4 * i + 2] = q.z, v.r[4 * i + 3] = q.w;
-      }
-    }
+    for (int i = 0; i < PIECES; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.r[4 * i]), "=r"(v.r[4 * i + 1]), "=r"(v.r[4 * i + 2]), "=r"(v.r[4 * i + 3])
+                   : "r"(mine + out + (k * PIECES + i) * kThreads * 16)
+                   : "memory");
     return v;
   }
-  __device__ __forceinline__ void next() {
-    if (++stage_out == STAGES) stage_out = 0;
-  }
+  __device__ __forceinline__ void next() { out = out + STAGE == END ? 0 : out + STAGE; }
 };
 
 // U: heads worked on at a time, an even number.
@@ -406,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
       const int lo = w.first(p, t), heads = w.last(p, t) - lo;
       if (heads <= 0) continue;
       T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + lo * x.out_h + me.chunk * 8;
+      const long long step = x.out_h;
       // y_i = r (x_i A_i + x'_i B_i), the weight folded into A and B
       F2 A[8], B[8];
 #pragma unroll
@@ -423,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
         feed.wait();
         Row8<T> now[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) now[k] = feed.row(k, live && h0 + k < heads);
+        for (int k = 0; k < U; ++k) now[k] = feed.row(k);
         feed.next();
         feed.load(p, ROWS, me.lane_row, me.chunk, me.in_row);
         F2 o[U / 2][8], r[U / 2];
@@ -455,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
           float a[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) a[i] = k & 1 ? split2(o[k / 2][i]).y : split2(o[k / 2][i]).x;
-          if (live && h0 + k < heads) store8(dst + (h0 + k) * x.out_h, a);
+          if (live && h0 + k < heads) store8(dst, a);
+          dst += step;
         }
       }
     }
@@ -494,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
       const int lo = w.first(p, t), heads = w.last(p, t) - lo;
       if (heads <= 0) continue;
       T* dst = static_cast<T*>(x.out) + w.b * x.out_b + n * x.out_n + lo * x.out_h + me.chunk * 8;
+      const long long step = x.out_h;
       float wt[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) wt[i] = x.w && me.in_row ? x.w[me.chunk * 8 + i] : 1.f;
@@ -507,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
         feed.wait();
         {
           F2 d[8], o[8];
-          const Row8<T> d0 = feed.row(2, live), d1 = feed.row(3, second);
-          unpack_pair(feed.row(0, live), feed.row(1, second), v);
+          const Row8<T> d0 = feed.row(2), d1 = feed.row(3);
+          unpack_pair(feed.row(0), feed.row(1), v);
           feed.next();
           feed.load(p, ROWS, me.lane_row, me.chunk, me.in_row);
           unpack_pair(d0, d1, d);
@@ -540,8 +560,10 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
           const float2 f = split2(v[i]);
           a[i] = f.x, b[i] = f.y;
         }
-        if (live) store8(dst + h0 * x.out_h, a);
-        if (second) store8(dst + (h0 + 1) * x.out_h, b);
+        if (live) store8(dst, a);
+        dst += step;
+        if (second) store8(dst, b);
+        dst += step;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
