@@ -27,24 +27,28 @@ struct Tiling {
 // SM gets of the L2's rate) plus the start of a tile, and at the end there is
 // an epilogue. The last round's tiles are too few for all pairs and are split
 // along the contraction, which costs a second kernel that reads the parts.
-// `wide` excludes bn = 192 where a tile's second half would start inside a
-// head.
+// `wide` allows only tiles whose second half of columns does not start inside
+// a head.
 Tiling choose(long long batches, long long rows, long long cols, long long kblocks, int sms, bool wide) {
   const long long pairs = sms / 2;
   Tiling best{};
   double best_cost = -1;
-  for (int bn : {256, 192, 128}) {
-    if (wide && bn == 192) continue;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    if (wide && bn % 128) continue;
     const long long tiles = batches * ceil_div(rows, 256) * ceil_div(cols, bn), whole = tiles / pairs * pairs;
     const long long rest = tiles - whole;
     const double load = (16384 + 64.0 * bn) / 47, step = load > 2.0 * bn ? load : 2.0 * bn;
     const double base = whole / pairs * (kblocks * step + 800) + 12.0 * bn;
-    for (int s = 1; s <= 32 && s <= kblocks && (s == 1 || rest * (s - 1) < pairs); ++s) {
+    const long long fill = rest ? pairs / rest : 1;  // parts that give every pair one
+    for (long long s : {1LL, fill / 2, fill}) {
+      if (s > 32) s = 32;
+      if (s > kblocks) s = kblocks;
+      if (s < 1) continue;
       double cost = base + ceil_div(rest * s, pairs) * (ceil_div(kblocks, s) * step + 800);
       if (s > 1) cost += 5000 + 8.0 * s * rest * 256 * bn / 2700;
       if (best_cost < 0 || cost < best_cost) {
         best_cost = cost;
-        best = s > 1 ? Tiling{bn, s, whole, rest} : Tiling{bn, 1, tiles, 0};
+        best = s > 1 ? Tiling{bn, (int)s, whole, rest} : Tiling{bn, 1, tiles, 0};
       }
     }
   }

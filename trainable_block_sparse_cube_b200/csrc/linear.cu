@@ -31,6 +31,8 @@
 #include <type_traits>
 
 #include "pair_ptx.cuh"
+#include "packed.cuh"
+#include "behind.cuh"
 #include "vsa_common.cuh"
 
 namespace vsa {
@@ -76,6 +78,11 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <typename T>
+__device__ __forceinline__ F2 packed2(uint32_t v) {
+  const float2 f = unpack2<T>(v);
+  return pair2(f.x, f.y);
 }
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
@@ -337,6 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  ptx::wait_for_previous();
+  ptx::let_next_start();
 
   // The two issuing warps run their loops as whole warps, so that what they
   // compute is uniform, and elect a lane to issue.
@@ -442,11 +451,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       }
     }
   } else {
-    // ---- epilogue: a warp takes 32 rows, a row a lane, and every second
-    // 64-column group of the tile, from tensor memory straight to global memory
+    // ---- epilogue: a warp takes 32 rows, a row a lane, and one half of the tile's
+    // columns, 32 at a time, from tensor memory straight to global memory
     // in whole 32-byte sectors. Shared memory has no bandwidth to spare: the
     // MMAs read 64 bytes a cycle of it and the loads write as many (%STG%).
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, groups = p.bn / 32;
+    const int g0 = warp < 6 ? 0 : (groups + 1) / 2, g1 = warp < 6 ? (groups + 1) / 2 : groups;
     int tile = 0;
     for (unsigned u = pair; u < units; u += pairs, ++tile) {
       const Unit w(p, u);
@@ -455,62 +465,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       tc_fence_after();
       const int in_tile = (int)rank * 128 + quarter * 32 + lane, n = w.row0 + in_tile;
       const bool live = n < p.rows;
-      for (int g = (warp - 2) >> 2; g * 64 < p.bn; g += 2) {
-        const int col = w.col0 + g * 64;
-        if (n - lane >= p.rows || col >= p.F) break;
-        const int head = col / p.out.D, c = col - head * p.out.D;
 #pragma unroll 1
-        for (int h = 0; h < 2 && col + 32 * h < p.F; ++h) {
-          uint32_t r[32];
-          const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 64 + 32 * h);
-          if (w.part >= 0) {  // a part of the contraction: fp32 sums
-            tmem_ld32(acc, r);
-            tmem_wait_ld();
-            float* const dst = p.partial + ((long long)w.part * 256 + in_tile) * p.bn + g * 64 + 32 * h;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = r[8 * j + i];
-              if (live) store32(dst + 8 * j, v, p.wide, true);
-            }
-            continue;
-          }
-          const int ch = c + 32 * h, left = p.F - (col + 32 * h);  // columns up to the edge, a multiple of 8
-          uint32_t x[2][8];
-          if (p.residual.data) {
-            const T* const src = view_at<T>(p.residual, w.batch, head, n) + ch;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (live && 16 * j < left) load32(src + 16 * j, x[j], p.wide, left > 16 * j + 8);
-          }
+      for (int g = g0; g < g1; ++g) {
+        const int col = w.col0 + g * 32, left = p.F - col;  // columns up to the edge, a multiple of 8
+        if (n - lane >= p.rows || left <= 0) break;
+        uint32_t r[32];
+        const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 32);
+        if (w.part >= 0) {  // a part of the contraction: fp32 sums
           tmem_ld32(acc, r);
           tmem_wait_ld();
+          float* const dst = p.partial + ((long long)w.part * 256 + in_tile) * p.bn + g * 32;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (16 * j >= left) break;
-            const bool both = left > 16 * j + 8;
-            float v[16];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
-            if (p.bias) add_bias16(v, p.bias + col + 32 * h + 16 * j, both);
-            uint32_t o[8];
-            if (p.z.data) {
-              pack16<T>(v, o);
-              if (live) store32(view_at<T>(p.z, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
-            }
-            activate_n(v, p.act);
-            if (p.residual.data) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 f = unpack2<T>(x[j][i]);
-                v[2 * i] += f.x;
-                v[2 * i + 1] += f.y;
-              }
-            }
-            pack16<T>(v, o);
-            if (live) store32(view_at<T>(p.out, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
+            for (int i = 0; i < 8; ++i) v[i] = r[8 * j + i];
+            if (live) store32(dst + 8 * j, v, p.wide, true);
           }
+          continue;
+        }
+        const int head = p.out.heads > 1 ? col / p.out.D : 0, ch = col - head * p.out.D;
+        uint32_t x[2][8];
+        if (p.residual.data) {
+          const T* const src = view_at<T>(p.residual, w.batch, head, n) + ch;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (live && 16 * j < left) load32(src + 16 * j, x[j], p.wide, left > 16 * j + 8);
+        }
+        tmem_ld32(acc, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (16 * j >= left) break;
+          const bool both = left > 16 * j + 8;
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
+          if (p.bias) add_bias16(v, p.bias + col + 16 * j, both);
+          uint32_t o[8];
+          if (p.z.data) {
+            pack16<T>(v, o);
+            if (live) store32(view_at<T>(p.z, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
+          }
+          activate_n(v, p.act);
+          if (p.residual.data) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 f = unpack2<T>(x[j][i]);
+              v[2 * i] += f.x;
+              v[2 * i + 1] += f.y;
+            }
+          }
+          pack16<T>(v, o);
+          if (live) store32(view_at<T>(p.out, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
         }
       }
       tc_fence_before();
@@ -529,6 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
 // out = act(sum of the parts + bias) + residual of the split tiles, 8 columns a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
+  ptx::wait_for_previous();
   const int groups = p.bn / 8, per_tile = 256 * groups;
   const int tile = blockIdx.x / (per_tile / 256), in = (blockIdx.x % (per_tile / 256)) * 256 + threadIdx.x;
   int rt, ct;
@@ -561,20 +569,23 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
 // ---------------------------------------------------------------- few rows
 constexpr int kSkinnyK = 2048;  // channels of x staged at a time
 
-// R >= batches * rows rows; a warp computes two columns of all of them, its
-// lanes 8 channels apart along W's row.
-template <int R, typename T>
+// R >= batches * rows rows; a warp computes FO columns of all of them, its
+// lanes 8 channels apart along W's row, even and odd channels in the halves of
+// a packed sum. Eight rows take four columns at a time: their reads of x from
+// shared memory, not W's, bound them otherwise (8 x 1536 x 9216: %SK0% us with
+// two columns, %SK1% with four).
+template <int R, int FO, typename T>
 __global__ void __launch_bounds__(256) skinny_kernel(const SkinnyParams p) {
   __shared__ uint4 xs[R][kSkinnyK / 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int M = p.batches * p.rows;
-  const int f0 = (blockIdx.x * 8 + warp) * 2;
-  float acc[2][R];
+  const int f0 = (blockIdx.x * 8 + warp) * FO;
+  F2 acc[FO][R];
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < FO; ++f)
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[f][r] = 0.f;
-  const T* const w = static_cast<const T*>(p.w);
+    for (int r = 0; r < R; ++r) acc[f][r] = 0;
+  const T* const w = static_cast<const T*>(p.w) + (long long)f0 * p.w_stride;
   for (int k0 = 0; k0 < p.K; k0 += kSkinnyK) {
     const int len = min(kSkinnyK, p.K - k0) / 8;
     if (k0) __syncthreads();
@@ -583,21 +594,23 @@ __global__ void __launch_bounds__(256) skinny_kernel(const SkinnyParams p) {
       xs[r][c] = r < M ? *reinterpret_cast<const uint4*>(at<T>(p.x, r / p.rows, r % p.rows, k0 + c * 8)) : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
-    if (f0 < p.F) {  // F is a multiple of 8: both columns lie inside
-#pragma unroll 4
+    if (f0 < p.F) {  // F is a multiple of 8: all columns lie inside
+#pragma unroll 2
       for (int c = lane; c < len; c += 32) {
-        float a[2][8];
+        F2 a[FO][4];
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-          unpack8<T>(__ldg(reinterpret_cast<const uint4*>(w + (f0 + f) * p.w_stride + k0) + c), a[f]);
+        for (int f = 0; f < FO; ++f) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + f * p.w_stride + k0) + c);
+          a[f][0] = packed2<T>(q.x), a[f][1] = packed2<T>(q.y), a[f][2] = packed2<T>(q.z), a[f][3] = packed2<T>(q.w);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float x[8];
-          unpack8<T>(xs[r][c], x);
+          const uint4 q = xs[r][c];
+          const F2 x[4] = {packed2<T>(q.x), packed2<T>(q.y), packed2<T>(q.z), packed2<T>(q.w)};
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
+          for (int f = 0; f < FO; ++f)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[f][r] = fmaf(a[f][i], x[i], acc[f][r]);
+            for (int i = 0; i < 4; ++i) acc[f][r] = fma2(a[f][i], x[i], acc[f][r]);
         }
       }
     }
@@ -605,15 +618,17 @@ __global__ void __launch_bounds__(256) skinny_kernel(const SkinnyParams p) {
   if (f0 >= p.F) return;
   float mine = 0.f;
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < FO; ++f)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const float2 h = split2(acc[f][r]);
+      float v = h.x + h.y;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) acc[f][r] += __shfl_xor_sync(0xffffffffu, acc[f][r], o);
-      if (lane == f * R + r) mine = acc[f][r];
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == f * R + r) mine = v;
     }
   const int f = lane / R, r = lane % R;
-  if (f < 2 && r < M) {
+  if (f < FO && r < M) {
     const int c = f0 + f, b = r / p.rows, n = r % p.rows;
     if (p.bias) mine += p.bias[c];
     if (p.z.data) *at<T>(p.z, b, n, c) = static_cast<T>(mine);
@@ -631,6 +646,7 @@ __global__ void __launch_bounds__(256) skinny_kernel(const SkinnyParams p) {
 template <typename T>
 __global__ void __launch_bounds__(256) slope_kernel(const SlopeParams p) {
   __shared__ float part[8][32][9];
+  ptx::let_next_start();
   const int tx = threadIdx.x, ty = threadIdx.y;
   const int c = (blockIdx.x * 32 + tx) * 8;
   const unsigned M = (unsigned)p.batches * p.rows;
@@ -669,6 +685,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeParams p) {
 
 // db = sum of the blocks' column sums, 32 columns a block, always in the same order.
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* partial, int blocks, int F, float* db) {
+  ptx::wait_for_previous();
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
@@ -696,8 +713,7 @@ cudaError_t launch_gemm(const GemmParams& p, int num_sms, cudaStream_t st) {
     if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
   }
   const long long pairs = p.units < num_sms / 2 ? p.units : num_sms / 2;
-  gemm_kernel<KIND, T><<<(unsigned)(2 * pairs), kThreads, kGemmSmem, st>>>(p);
-  return cudaGetLastError();
+  return launch_behind(gemm_kernel<KIND, T>, dim3((unsigned)(2 * pairs)), dim3(kThreads), kGemmSmem, st, p);
 }
 
 template <typename T>
@@ -707,14 +723,18 @@ cudaError_t launch_gemm_kind(const GemmParams& p, int kind, int num_sms, cudaStr
   return launch_gemm<kGemmWeight, T>(p, num_sms, st);
 }
 
+template <int R, int FO, typename T>
+cudaError_t launch_skinny_rows(const SkinnyParams& p, cudaStream_t st) {
+  skinny_kernel<R, FO, T><<<(p.F + 8 * FO - 1) / (8 * FO), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t launch_skinny(const SkinnyParams& p, cudaStream_t st) {
-  const int M = p.batches * p.rows, blocks = (p.F + 15) / 16;
-  if (M <= 1) skinny_kernel<1, T><<<blocks, 256, 0, st>>>(p);
-  else if (M <= 2) skinny_kernel<2, T><<<blocks, 256, 0, st>>>(p);
-  else if (M <= 4) skinny_kernel<4, T><<<blocks, 256, 0, st>>>(p);
-  else skinny_kernel<8, T><<<blocks, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  const int M = p.batches * p.rows;
+  if (M <= 1) return launch_skinny_rows<1, 2, T>(p, st);
+  if (M <= 2) return launch_skinny_rows<2, 2, T>(p, st);
+  if (M <= 4) return launch_skinny_rows<4, 2, T>(p, st);
+  return launch_skinny_rows<8, 4, T>(p, st);
 }
 
 }  // namespace
@@ -725,9 +745,8 @@ cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_
 
 cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t st) {
   const int grid = p.rest * (p.bn / 8);
-  if (type) finish_kernel<__half><<<grid, 256, 0, st>>>(p);
-  else finish_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return type ? launch_behind(finish_kernel<__half>, dim3(grid), dim3(256), 0, st, p)
+              : launch_behind(finish_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, p);
 }
 
 cudaError_t launch_linear_skinny(const SkinnyParams& p, int type, cudaStream_t st) {
@@ -740,8 +759,8 @@ cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaS
   else slope_kernel<__nv_bfloat16><<<grid, block, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;
-  column_sum_kernel<<<(p.F + 31) / 32, dim3(32, 32), 0, st>>>(p.partial, p.blocks_y, p.F, db);
-  return cudaGetLastError();
+  return launch_behind(column_sum_kernel, dim3((p.F + 31) / 32), dim3(32, 32), 0, st, (const float*)p.partial, p.blocks_y,
+                       p.F, db);
 }
 
 cudaError_t linear_error_word(int* word, cudaStream_t st) {

@@ -30,6 +30,8 @@
 // order: no atomics, the same bits every time.
 #include <cuda_fp16.h>
 
+#include "behind.cuh"
+#include "packed.cuh"
 #include "sm100_ptx.cuh"
 #include "vsa_common.cuh"
 
@@ -108,35 +110,6 @@ __device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-
-// Two fp32 values in one register pair: the same channel of two heads.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pair2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 split2(F2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 both(float v) { return pair2(v, v); }
 
 template <typename T>
 __device__ __forceinline__ void unpack_pair(const Row8<T>& a, const Row8<T>& b, F2 (&x)[8]) {
@@ -494,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
   Feed<T, 2, true, STAGES> feed;
+  ptx::let_next_start();
   feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
   stage_rotation(p, freq, axis);
   const float inv_d = 1.f / (float)p.D;
@@ -585,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* partial, int blocks, int D, float* dwq,
                                                                 float* dwk) {
   __shared__ float s[32][33];
+  ptx::wait_for_previous();
   const int d = blockIdx.x * 32 + threadIdx.x, t = blockIdx.y;
   float* dw = t ? dwk : dwq;
   if (!dw) return;
@@ -662,8 +637,8 @@ cudaError_t launch_norm_rope_backward(RopeParams p, int type, float* dwq, float*
   const int grid = plan_units(p, num_sms, kBackwardPerSm, kBackwardAngles);
   cudaError_t e = launch_any(p, type, true, grid, st);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  norm_weight_grad_kernel<<<dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, st>>>(p.partial, grid, p.D, dwq, dwk);
-  return cudaGetLastError();
+  return launch_behind(norm_weight_grad_kernel, dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, st, (const float*)p.partial, grid,
+                       p.D, dwq, dwk);
 }
 
 }  // namespace vsa

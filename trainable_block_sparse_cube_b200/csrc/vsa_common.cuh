@@ -208,7 +208,7 @@ struct GemmParams {
   float* partial;           // parts of split tiles [splits, rest, 256, bn]
   int wide;                 // out, residual, z and partial are accessed in aligned 32-byte pieces
   int a_d, b_d;             // channels of a head of A, B
-  int bn;                   // columns of a tile: 128, 192 or 256
+  int bn;                   // columns of a tile: a multiple of 32, 64 to 256
   int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
   int rows;                 // rows of a batch
   int F, col_tiles;         // columns

@@ -203,6 +203,10 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _stream():
     # what torch.cuda.current_stream().cuda_stream gives, without building the Stream object (3 us)
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -478,44 +482,27 @@ class Rotation:
         self._packed = bytes(self.spec)
 
 
-class _OnDevice:
-    """Makes the tensors' device current for the length of a call."""
-
-    def __init__(self, device):
-        self.device, self.before = device.index, None
-
-    def __enter__(self):
-        now = torch._C._cuda_getDevice()
-        if now != self.device:
-            self.before = now
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
+def _elsewhere(device):
+    """Whether another device than the tensors' is current (the call then starts again on theirs)."""
+    return torch._C._cuda_getDevice() != device.index
 
 
 def _need_heads(t, name, like=None, dtype=None, device=None):
-    """A CUDA tensor [B, heads, N, D] of any strides whose channels are contiguous."""
+    """Checks for a CUDA tensor [B, heads, N, D] of any strides whose channels are contiguous; its packed view."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have shape [B, heads, N, D], got {tuple(t.shape)}")
-    if t.dtype not in TYPES or (dtype is not None and t.dtype != dtype):
+    shape, s = t.shape, t.stride()
+    if len(s) != 4:
+        raise ValueError(f"{name} must have shape [B, heads, N, D], got {tuple(shape)}")
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in TYPES):
         raise ValueError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not {device}")
-    if like is not None and t.shape != like:
-        raise ValueError(f"{name} must have shape {tuple(like)}, got {tuple(t.shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if like is not None and shape != like:
+        raise ValueError(f"{name} must have shape {tuple(like)}, got {tuple(shape)}")
+    if s[3] != 1 and shape[3] > 1:
         raise ValueError(f"{name} must have contiguous channels")
-
-
-def _heads(t):
-    if t is None:
-        return None
-    s = t.stride()
-    return _pack_heads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
+    return _pack_heads(t.data_ptr(), shape[1], s[0], s[1], s[2])
 
 
 def _where(rotation, grid, origin, positions, B, N, device):
@@ -529,32 +516,33 @@ def _where(rotation, grid, origin, positions, B, N, device):
         if N != grid[0] * grid[1] * grid[2]:
             raise ValueError(f"N = {N} must equal T*H*W of grid {tuple(grid)}")
         return _pack_positions(*grid, *origin, 0, 0, 0)
-    p = positions
+    p, axes = positions, rotation.axes
     if not isinstance(p, torch.Tensor) or not p.is_cuda or p.device != device:
         raise ValueError(f"positions must be a CUDA tensor on {device}")
     if p.dtype not in (torch.int32, torch.float32):
         raise ValueError(f"positions must be int32 or float32, got {p.dtype}")
-    if p.dim() == 2:
-        p = p[None]
-    if tuple(p.shape) not in ((B, N, rotation.axes), (1, N, rotation.axes)):
-        raise ValueError(f"positions must have shape [{N}, {rotation.axes}] or [{B}, {N}, {rotation.axes}], "
-                         f"got {tuple(positions.shape)}")
-    if p.numel() and not p[0].is_contiguous():
+    shape, s = p.shape, p.stride()
+    if len(s) not in (2, 3) or shape[-2:] != (N, axes) or (len(s) == 3 and shape[0] not in (1, B)):
+        raise ValueError(f"positions must have shape [{N}, {axes}] or [{B}, {N}, {axes}], got {tuple(shape)}")
+    if N and ((axes > 1 and s[-1] != 1) or (N > 1 and s[-2] != axes)):
         raise ValueError("positions must be contiguous")
-    return _pack_positions(0, 0, 0, 0, 0, 0, p.data_ptr() if p.numel() else 16, 0 if p.dtype == torch.int32 else 1,
-                           p.stride(0) if p.shape[0] > 1 else 0)
+    return _pack_positions(0, 0, 0, 0, 0, 0, p.data_ptr() or 16, 0 if p.dtype == torch.int32 else 1,
+                           s[0] if len(s) == 3 and shape[0] > 1 else 0)
 
 
 def _sizes(q, k, rotation, names=("q", "k")):
-    _need_heads(q, names[0])
+    """(B, N, D, packed sizes, packed q, packed k)"""
+    hq = _need_heads(q, names[0])
     B, _, N, D = q.shape
     if rotation.D != D:
         raise ValueError(f"the rotation is for {rotation.D} channels, {names[0]} has {D}")
+    hk = None
     if k is not None:
-        _need_heads(k, names[1], dtype=q.dtype, device=q.device)
-        if (k.shape[0], k.shape[2], k.shape[3]) != (B, N, D):
-            raise ValueError(f"{names[1]} must have shape [{B}, heads, {N}, {D}], got {tuple(k.shape)}")
-    return B, N, D, _pack_rope_sizes(TYPES[q.dtype], B, N, D)
+        hk = _need_heads(k, names[1], None, q.dtype, q.device)
+        s = k.shape
+        if s[0] != B or s[2] != N or s[3] != D:
+            raise ValueError(f"{names[1]} must have shape [{B}, heads, {N}, {D}], got {tuple(s)}")
+    return B, N, D, _pack_rope_sizes(TYPES[q.dtype], B, N, D), hq, hk
 
 
 def _need_weight(w, name, D, device):
@@ -564,19 +552,17 @@ def _need_weight(w, name, D, device):
             raise ValueError(f"{name} is on {w.device}, not {device}")
 
 
-def _outputs(q, k, q_out, k_out, names, like_input=False):
-    """The given outputs, checked, or new ones: contiguous, or in the inputs' order of dimensions."""
-    out = []
-    for t, o, name in ((q, q_out, names[0]), (k, k_out, names[1])):
-        if t is None:
-            if o is not None:
-                raise ValueError(f"{name} has no input")
-        elif o is None:
-            o = torch.empty_like(t) if like_input else torch.empty_like(t, memory_format=torch.contiguous_format)
-        else:
-            _need_heads(o, name, like=t.shape, dtype=t.dtype, device=t.device)
-        out.append(o)
-    return out
+def _output(t, o, name, like_input=False):
+    """The given output, checked, or a new one (contiguous, or in its input's order of dimensions), and its view."""
+    if t is None:
+        if o is not None:
+            raise ValueError(f"{name} has no input")
+        return None, None
+    if o is None:
+        o = torch.empty_like(t) if like_input else torch.empty_like(t, memory_format=torch.contiguous_format)
+        s = o.stride()
+        return o, _pack_heads(o.data_ptr(), o.shape[1], s[0], s[1], s[2])
+    return o, _need_heads(o, name, t.shape, t.dtype, t.device)
 
 
 def rope(q, k, rotation, grid=None, origin=(0, 0, 0), positions=None, q_out=None, k_out=None):
@@ -584,24 +570,31 @@ def rope(q, k, rotation, grid=None, origin=(0, 0, 0), positions=None, q_out=None
     another number of heads). Tokens lie on the raster ``grid`` (T, H, W) from ``origin`` on, or at
     ``positions`` ([N, axes] or [B, N, axes], int32 or float32). Returns (q_out, k_out), contiguous unless
     given; an output may be its input. Enqueued on the current stream."""
-    B, N, D, sizes = _sizes(q, k, rotation)
-    where = _where(rotation, grid, origin, positions, B, N, q.device)
-    with _OnDevice(q.device):
-        q_out, k_out = _outputs(q, k, q_out, k_out, ("q_out", "k_out"))
-        _check(_load_projection().vsa_rope(sizes, rotation._packed, where, _heads(q), _heads(k), _heads(q_out),
-                                           _heads(k_out), _stream()), "vsa_rope")
+    B, N, _, sizes, hq, hk = _sizes(q, k, rotation)
+    device = q.device
+    where = _where(rotation, grid, origin, positions, B, N, device)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return rope(q, k, rotation, grid, origin, positions, q_out, k_out)
+    q_out, oq = _output(q, q_out, "q_out")
+    k_out, ok = _output(k, k_out, "k_out")
+    _check(_load_projection().vsa_rope(sizes, rotation._packed, where, hq, hk, oq, ok, _stream()), "vsa_rope")
     return q_out, k_out
 
 
 def rope_backward(dq_out, dk_out, rotation, grid=None, origin=(0, 0, 0), positions=None, dq=None, dk=None):
     """Gradients of rope's inputs from those of its outputs (dk_out may be None): (dq, dk), contiguous unless
     given. Enqueued on the current stream."""
-    B, N, _, sizes = _sizes(dq_out, dk_out, rotation, ("dq_out", "dk_out"))
-    where = _where(rotation, grid, origin, positions, B, N, dq_out.device)
-    with _OnDevice(dq_out.device):
-        dq, dk = _outputs(dq_out, dk_out, dq, dk, ("dq", "dk"))
-        _check(_load_projection().vsa_rope_backward(sizes, rotation._packed, where, _heads(dq_out), _heads(dk_out),
-                                                    _heads(dq), _heads(dk), _stream()), "vsa_rope_backward")
+    B, N, _, sizes, hq, hk = _sizes(dq_out, dk_out, rotation, ("dq_out", "dk_out"))
+    device = dq_out.device
+    where = _where(rotation, grid, origin, positions, B, N, device)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return rope_backward(dq_out, dk_out, rotation, grid, origin, positions, dq, dk)
+    dq, oq = _output(dq_out, dq, "dq")
+    dk, ok = _output(dk_out, dk, "dk")
+    _check(_load_projection().vsa_rope_backward(sizes, rotation._packed, where, hq, hk, oq, ok, _stream()),
+           "vsa_rope_backward")
     return dq, dk
 
 
@@ -609,15 +602,18 @@ def qk_norm_rope(q, k, q_weight, k_weight, rotation, grid=None, origin=(0, 0, 0)
                  q_out=None, k_out=None):
     """RMS norm of every head's queries and keys (weights [D] fp32 or None) and the rotation of ``rope`` in one
     pass; arguments, outputs and stream as there."""
-    B, N, D, sizes = _sizes(q, k, rotation)
-    where = _where(rotation, grid, origin, positions, B, N, q.device)
-    _need_weight(q_weight, "q_weight", D, q.device)
-    _need_weight(k_weight, "k_weight", D, q.device)
-    with _OnDevice(q.device):
-        q_out, k_out = _outputs(q, k, q_out, k_out, ("q_out", "k_out"))
-        _check(_load_projection().vsa_qk_norm_rope(sizes, rotation._packed, where, _heads(q), _heads(k),
-                                                   _ptr(q_weight), _ptr(k_weight), eps, _heads(q_out),
-                                                   _heads(k_out), _stream()), "vsa_qk_norm_rope")
+    B, N, D, sizes, hq, hk = _sizes(q, k, rotation)
+    device = q.device
+    where = _where(rotation, grid, origin, positions, B, N, device)
+    _need_weight(q_weight, "q_weight", D, device)
+    _need_weight(k_weight, "k_weight", D, device)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return qk_norm_rope(q, k, q_weight, k_weight, rotation, grid, origin, positions, eps, q_out, k_out)
+    q_out, oq = _output(q, q_out, "q_out")
+    k_out, ok = _output(k, k_out, "k_out")
+    _check(_load_projection().vsa_qk_norm_rope(sizes, rotation._packed, where, hq, hk, _address(q_weight),
+                                               _address(k_weight), eps, oq, ok, _stream()), "vsa_qk_norm_rope")
     return q_out, k_out
 
 
@@ -626,61 +622,61 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, rotation, gr
     """Gradients of qk_norm_rope from its inputs (nothing is saved) and the gradients of its outputs. Returns
     (dq, dk, dq_weight, dk_weight): dq and dk in the order of dimensions that q and k are stored in unless
     given, the weights' in fp32 (None where the weight is None). Enqueued on the current stream."""
-    B, N, D, sizes = _sizes(q, k, rotation)
-    where = _where(rotation, grid, origin, positions, B, N, q.device)
-    _need_weight(q_weight, "q_weight", D, q.device)
-    _need_weight(k_weight, "k_weight", D, q.device)
-    _need_heads(dq_out, "dq_out", like=q.shape, dtype=q.dtype, device=q.device)
+    B, N, D, sizes, hq, hk = _sizes(q, k, rotation)
+    device = q.device
+    where = _where(rotation, grid, origin, positions, B, N, device)
+    _need_weight(q_weight, "q_weight", D, device)
+    _need_weight(k_weight, "k_weight", D, device)
+    gq = _need_heads(dq_out, "dq_out", q.shape, q.dtype, device)
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out must be given together")
-    if k is not None:
-        _need_heads(dk_out, "dk_out", like=k.shape, dtype=q.dtype, device=q.device)
-    with _OnDevice(q.device):
-        L = _load_projection()
-        dq, dk = _outputs(q, k, dq, dk, ("dq", "dk"), like_input=True)
-        dwq = None if q_weight is None else torch.empty_like(q_weight)
-        dwk = None if k is None or k_weight is None else torch.empty_like(k_weight)
-        nb = L.vsa_qk_norm_rope_backward_workspace_bytes(D)
-        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
-        _check(L.vsa_qk_norm_rope_backward(sizes, rotation._packed, where, _heads(q), _heads(k), _ptr(q_weight),
-                                           _ptr(k_weight), eps, _heads(dq_out), _heads(dk_out), _heads(dq), _heads(dk),
-                                           _ptr(dwq), _ptr(dwk), _ptr(ws), nb, _stream()),
-               "vsa_qk_norm_rope_backward")
+    gk = None if k is None else _need_heads(dk_out, "dk_out", k.shape, q.dtype, device)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, rotation, grid, origin, positions,
+                                         eps, dq, dk)
+    L = _load_projection()
+    dq, oq = _output(q, dq, "dq", like_input=True)
+    dk, ok = _output(k, dk, "dk", like_input=True)
+    dwq = None if q_weight is None else torch.empty_like(q_weight)
+    dwk = None if k is None or k_weight is None else torch.empty_like(k_weight)
+    nb = L.vsa_qk_norm_rope_backward_workspace_bytes(D)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    _check(L.vsa_qk_norm_rope_backward(sizes, rotation._packed, where, hq, hk, _address(q_weight), _address(k_weight),
+                                       eps, gq, gk, oq, ok, _address(dwq), _address(dwk), ws.data_ptr(), nb,
+                                       _stream()), "vsa_qk_norm_rope_backward")
     return dq, dk, dwq, dwk
 
 
 def _need_rows(t, name, dtype=None, device=None, shape=None):
-    """A 16-bit CUDA tensor [B, N, channels] or [B, heads, N, D] whose channels are contiguous."""
+    """Checks for a 16-bit CUDA tensor [B, N, channels] or [B, heads, N, D] whose channels are contiguous; its
+    packed view as rows."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in (torch.bfloat16, torch.float16)):
         raise ValueError(f"{name} must be {dtype or 'bfloat16 or float16'}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{name} must have shape [B, N, channels] or [B, heads, N, D], got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    size, s = t.shape, t.stride()
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
+    if len(s) not in (3, 4):
+        raise ValueError(f"{name} must have shape [B, N, channels] or [B, heads, N, D], got {tuple(size)}")
+    if s[-1] != 1 and size[-1] > 1:
         raise ValueError(f"{name} must have contiguous channels")
-
-
-def _rows(t):
-    if t is None:
-        return None
-    s = t.stride()
     if len(s) == 3:
         return _pack_heads(t.data_ptr(), 1, s[0], 0, s[1])
-    return _pack_heads(t.data_ptr(), t.shape[1], s[0], s[1], s[2])
+    return _pack_heads(t.data_ptr(), size[1], s[0], s[1], s[2])
 
 
 def _linear_sizes(x, weight, activation):
-    _need_rows(x, "x")
+    """(B, N, F, packed sizes, packed x)"""
+    hx = _need_rows(x, "x")
     shape = x.shape
     B, N, K = shape if len(shape) == 3 else (shape[0], shape[2], shape[1] * shape[3])
     if not isinstance(weight, torch.Tensor) or not weight.is_cuda or weight.device != x.device:
         raise ValueError(f"weight must be a CUDA tensor on {x.device}")
-    if weight.dtype != x.dtype:
+    if weight.dtype is not x.dtype:
         raise ValueError(f"weight must be {x.dtype}, got {weight.dtype}")
     if weight.dim() != 2 or weight.shape[1] != K:
         raise ValueError(f"weight must have shape [F, {K}], got {tuple(weight.shape)}")
@@ -688,7 +684,8 @@ def _linear_sizes(x, weight, activation):
         raise ValueError("weight must have contiguous rows")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    return B, N, weight.shape[0], _pack_linear_sizes(TYPES[x.dtype], B, N, K, weight.shape[0])
+    F = weight.shape[0]
+    return B, N, F, _pack_linear_sizes(TYPES[x.dtype], B, N, K, F), hx
 
 
 def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out=None, z=None):
@@ -698,27 +695,31 @@ def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out
     [B, heads, N, F / heads] if ``heads`` is given; ``residual``, ``out`` and ``z`` (which receives
     x weight^T + bias for linear_backward) have that shape. out may be the residual. Enqueued on the current
     stream."""
-    B, N, F, sizes = _linear_sizes(x, weight, activation)
-    device = x.device
+    B, N, F, sizes, hx = _linear_sizes(x, weight, activation)
+    device, dtype = x.device, x.dtype
     if bias is not None:
         _need_weight(bias, "bias", F, device)
     if heads is None:
-        shape = torch.Size((B, N, F))
+        shape = (B, N, F)
     elif heads < 1 or F % heads:
         raise ValueError(f"{F} channels do not split into {heads} heads")
     else:
-        shape = torch.Size((B, heads, N, F // heads))
-    for t, name in ((residual, "residual"), (out, "out"), (z, "z")):
-        if t is not None:
-            _need_rows(t, name, x.dtype, device, shape)
-    with _OnDevice(device):
-        L = _load_projection()
-        if out is None:
-            out = x.new_empty(shape)
-        nb = L.vsa_linear_workspace_bytes(sizes)
-        ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
-        _check(L.vsa_linear(sizes, _rows(x), weight.data_ptr(), weight.stride(0), _ptr(bias), ACTIVATIONS[activation],
-                            _rows(residual), _rows(z), _rows(out), _ptr(ws), nb, _stream()), "vsa_linear")
+        shape = (B, heads, N, F // heads)
+    hr = None if residual is None else _need_rows(residual, "residual", dtype, device, shape)
+    hz = None if z is None else _need_rows(z, "z", dtype, device, shape)
+    ho = None if out is None else _need_rows(out, "out", dtype, device, shape)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return linear(x, weight, bias, activation, residual, heads, out, z)
+    L = _load_projection()
+    if out is None:
+        out = x.new_empty(shape)
+        ho = _pack_heads(out.data_ptr(), 1, N * F, 0, F) if heads is None else \
+            _pack_heads(out.data_ptr(), heads, N * F, N * shape[3], shape[3])
+    nb = L.vsa_linear_workspace_bytes(sizes)
+    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _check(L.vsa_linear(sizes, hx, weight.data_ptr(), weight.stride(0), _address(bias), ACTIVATIONS[activation], hr, hz,
+                        ho, _address(ws), nb, _stream()), "vsa_linear")
     return out
 
 
@@ -727,35 +728,34 @@ def linear_backward(x, weight, dout, z=None, activation=None, bias=False, dx=Non
     stored, needed with an activation; dbias (fp32) is None unless ``bias``; ``want`` switches dx and dweight
     off. dx is in the order of dimensions that x is stored in unless given. The residual's gradient is dout.
     Enqueued on the current stream."""
-    B, N, F, sizes = _linear_sizes(x, weight, activation)
-    device = x.device
-    _need_rows(dout, "dout", x.dtype, device)
+    B, N, F, sizes, hx = _linear_sizes(x, weight, activation)
+    device, dtype = x.device, x.dtype
+    hg = _need_rows(dout, "dout", dtype, device)
     s = dout.shape
     if (s if len(s) == 3 else (s[0], s[2], s[1] * s[3])) != (B, N, F):
-        raise ValueError(f"dout must have shape [{B}, {N}, {F}] or [{B}, heads, {N}, D], "
-                         f"got {tuple(s)}")
-    if activation is not None:
-        _need_rows(z, "z", x.dtype, device, s)
-    if dx is not None:
-        _need_rows(dx, "dx", x.dtype, device, x.shape)
-    with _OnDevice(device):
-        L = _load_projection()
-        if want[0] and dx is None:
-            dx = torch.empty_like(x)
-        dw = torch.empty_like(weight, memory_format=torch.contiguous_format) if want[1] else None
-        db = torch.empty(F, dtype=torch.float32, device=device) if bias else None
-        nb = L.vsa_linear_backward_workspace_bytes(sizes, ACTIVATIONS[activation])
-        ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
-        _check(L.vsa_linear_backward(sizes, _rows(x), weight.data_ptr(), weight.stride(0),
-                                     _rows(z) if activation is not None else None, ACTIVATIONS[activation],
-                                     _rows(dout), _rows(dx) if want[0] else None, _ptr(dw), _ptr(db), _ptr(ws), nb,
-                                     _stream()), "vsa_linear_backward")
-    return (dx if want[0] else None), dw, db
+        raise ValueError(f"dout must have shape [{B}, {N}, {F}] or [{B}, heads, {N}, D], got {tuple(s)}")
+    hz = None if activation is None else _need_rows(z, "z", dtype, device, s)
+    hd = None if dx is None else _need_rows(dx, "dx", dtype, device, x.shape)
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return linear_backward(x, weight, dout, z, activation, bias, dx, want)
+    L = _load_projection()
+    if not want[0]:
+        dx = hd = None
+    elif dx is None:
+        dx = torch.empty_like(x)
+        hd = _need_rows(dx, "dx")
+    dw = torch.empty_like(weight, memory_format=torch.contiguous_format) if want[1] else None
+    db = torch.empty(F, dtype=torch.float32, device=device) if bias else None
+    nb = L.vsa_linear_backward_workspace_bytes(sizes, ACTIVATIONS[activation])
+    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    _check(L.vsa_linear_backward(sizes, hx, weight.data_ptr(), weight.stride(0), hz, ACTIVATIONS[activation], hg, hd,
+                                 _address(dw), _address(db), _address(ws), nb, _stream()), "vsa_linear_backward")
+    return dx, dw, db
 
 
 def linear_check(device=None):
     """Synchronises the current stream of the device and raises VSAError if a wait inside a linear product on it
     gave up since the last check."""
-    device = torch.device("cuda" if device is None else device)
-    with _OnDevice(torch.device("cuda", torch.cuda.current_device()) if device.index is None else device):
+    with torch.cuda.device(device):
         _check(load().vsa_linear_check(_stream()), "vsa_linear_check")
