@@ -99,7 +99,12 @@ CASES = [
     (1, 3, 8, 8, 0, 0, "gelu_tanh", True, True, "rows"),
     (3, 2, 640, 24, 5, 0, None, True, True, "slice"),
     (2, 4, 128, 128, 2, 2, "silu", False, True, "heads"),
-    (1, 9, 8, 8, 0, 0, None, True, False, "rows"),                   # tensor cores from here on
+    (1, 9, 8, 8, 0, 0, None, True, False, "rows"),                   # two groups of eight rows
+    (5, 3, 1096, 1000, 0, 0, "gelu", True, True, "slice"),
+    (4, 4, 2048, 144, 16, 0, "silu", True, False, "heads"),
+    (1, 17, 136, 72, 0, 0, "gelu_tanh", True, True, "rows"),         # tiles from here on
+    (1, 17, 8, 8, 0, 0, None, True, False, "rows"),
+    (3, 7, 64, 192, 1, 3, None, False, False, "heads"),              # batches that are no run of rows
     (9, 1, 512, 256, 4, 2, "silu", True, True, "heads"),
     (1, 40, 4096, 256, 0, 0, "gelu_tanh", True, True, "rows"),       # a split contraction
     (2, 37, 1096, 392, 0, 0, "gelu", True, True, "slice"),

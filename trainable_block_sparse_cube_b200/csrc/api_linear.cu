@@ -102,7 +102,7 @@ Product weight_product(const vsa_linear_sizes* s, bool join, bool wide) {
   return p;
 }
 
-bool skinny(const vsa_linear_sizes* s) { return (long long)s->B * s->N <= vsa::kSkinnyRows; }
+bool few_rows(const vsa_linear_sizes* s) { return (long long)s->B * s->N <= vsa::kFewRows; }
 
 int slope_blocks(long long M, int F, int sms) {
   const long long strips = ceil_div(F, 256), rows = ceil_div(M, 8), most = 8LL * sms / strips;
@@ -184,7 +184,8 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   const bool weight = p.kind == vsa::kGemmWeight;
   const long long runs = weight ? p.kblocks / p.kblocks_batch : p.batches, run_rows = weight ? b_rows : p.rows;
   const int half = p.t.bn / 2;
-  vsa_status e = encode(&g.ta, a, run_rows, runs, weight ? 64 : 128, type);
+  g.a_rows = p.rows < 128 ? (int)ceil_div(p.rows, 8) * 8 : 128;
+  vsa_status e = encode(&g.ta, a, run_rows, runs, weight ? 64 : g.a_rows, type);
   if (e == VSA_OK) e = encode(&g.tb, b, b_rows, weight ? runs : 1, p.kind == vsa::kGemmForward ? half : 64, type);
   if (e != VSA_OK) return e;
   g.out = ep.out;
@@ -291,7 +292,7 @@ extern "C" {
 size_t vsa_linear_workspace_bytes(const vsa_linear_sizes* sizes) {
   int sms = 0;
   if (check_sizes(sizes) != VSA_OK || vsa::current_device_sms(&sms) != VSA_OK) return 0;
-  if (!sizes->B || !sizes->N || skinny(sizes)) return 0;
+  if (!sizes->B || !sizes->N || few_rows(sizes)) return 0;
   size_t n = 0;
   for (bool join : {false, true}) {
     Product p = forward_product(sizes, join);
@@ -330,8 +331,8 @@ vsa_status vsa_linear(const vsa_linear_sizes* sizes, const vsa_heads* x, const v
   out = single_token(out, swap, store + 3);
   Epilogue ep{bias, activation, rows_view(residual, sizes->F), rows_view(z, sizes->F), rows_view(out, sizes->F)};
   const RowsView xv = rows_view(x, sizes->K);
-  if (skinny(sizes)) {
-    vsa::SkinnyParams p{};
+  if (few_rows(sizes)) {
+    vsa::FewRowsParams p{};
     p.x = xv;
     p.residual = ep.residual;
     p.z = ep.z;
@@ -344,7 +345,7 @@ vsa_status vsa_linear(const vsa_linear_sizes* sizes, const vsa_heads* x, const v
     p.batches = sizes->B;
     p.K = sizes->K;
     p.F = sizes->F;
-    return vsa::launch_linear_skinny(p, sizes->type, st) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
+    return vsa::launch_linear_few_rows(p, sizes->type, st) == cudaSuccess ? VSA_OK : VSA_ERR_CUDA;
   }
   Product p = forward_product(sizes, joined(sizes->B, sizes->N, {x, residual, z, out}));
   p.plan(sms);

@@ -19,8 +19,8 @@
 //    large.
 //  * finish_kernel joins the parts of a contraction that was split because it
 //    has too few tiles for 74 pairs, always in the same order.
-//  * skinny_kernel, up to 8 rows: a warp a pair of output columns, bound by
-//    the one pass over W.
+//  * few_rows_kernel, up to %FEW% rows: W straight from memory into warp-wide
+//    MMAs, bound by the one pass over W.
 //
 // Sums are fp32; the result is rounded once. dz is rounded to the operands'
 // type before its products, as the tensor cores read it; db is summed from
@@ -31,7 +31,6 @@
 #include <type_traits>
 
 #include "pair_ptx.cuh"
-#include "packed.cuh"
 #include "behind.cuh"
 #include "vsa_common.cuh"
 
@@ -78,11 +77,6 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
 template <>
 __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
-template <typename T>
-__device__ __forceinline__ F2 packed2(uint32_t v) {
-  const float2 f = unpack2<T>(v);
-  return pair2(f.x, f.y);
 }
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
@@ -353,7 +347,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     // ---- loads of this CTA's operand rows; both CTAs' complete on the even CTA's barriers
     const int b_boxes = (half + 63) / 64;
     const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : b_boxes * 8192;
-    const uint32_t pair_bytes = 2 * (kTileA + b_bytes);
     const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
     const bool load = p.stall == 0;
     Ring ring;
@@ -378,6 +371,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         k = w.k0 * 64 - kh * p.a_d;
         kend = p.a_d;
       }
+      // What a CTA whose rows lie behind the last computes is not stored: it
+      // loads none, and a few rows are loaded as a smaller box (boxes of 128
+      // rows with fewer than 16 inside the tensor are slow: 9 x 4096 x 4096
+      // %BX%).
+      const bool load_a = KIND == kGemmWeight || row < p.rows;
+      const uint32_t a_bytes = KIND == kGemmWeight ? kTileA : p.a_rows * 128;
+      const uint32_t pair_bytes = 2 * b_bytes + (KIND == kGemmWeight || w.row0 + 128 < p.rows ? 2 : 1) * a_bytes;
       for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
         const int s = ring.stage;
         ok = wait.warp(&sh.empty[s], ring.parity ^ 1);  // passes at once where no use came before
@@ -393,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
               tma_load_4d_pair(a + 8192, &p.ta, bar, cc1, k, ch1, kh);
               if (b_boxes > 1) tma_load_4d_pair(b + 8192, &p.tb, bar, bc1, k, bh1, kh);
             } else {
-              tma_load_4d_pair(a, &p.ta, bar, k, row, kh, w.batch);
+              if (load_a) tma_load_4d_pair(a, &p.ta, bar, k, row, kh, w.batch);
               if (KIND == kGemmForward) {
                 tma_load_4d_pair(b, &p.tb, bar, kb * 64, col, 0, 0);
               } else {
@@ -567,76 +567,95 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
 }
 
 // ---------------------------------------------------------------- few rows
-constexpr int kSkinnyK = 2048;  // channels of x staged at a time
+constexpr int kFewWarps = 8, kFewColumns = 16;
 
-// R >= batches * rows rows; a warp computes FO columns of all of them, its
-// lanes 8 channels apart along W's row, even and odd channels in the halves of
-// a packed sum. Eight rows take four columns at a time: their reads of x from
-// shared memory, not W's, bound them otherwise (8 x 1536 x 9216: %SK0% us with
-// two columns, %SK1% with four).
-template <int R, int FO, typename T>
-__global__ void __launch_bounds__(256) skinny_kernel(const SkinnyParams p) {
-  __shared__ uint4 xs[R][kSkinnyK / 8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int M = p.batches * p.rows;
-  const int f0 = (blockIdx.x * 8 + warp) * FO;
-  F2 acc[FO][R];
+// D += A B with A [16 x 16] (W's rows), B [16 x 8] (x's rows as columns).
+template <typename T>
+__device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if (std::is_same<T, __half>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 * NT >= batches * rows rows; a block computes 16 columns of all of them,
+// its warps' shares of the contraction joined in shared memory, in order. W is
+// read once, straight into the fragments of a warp-wide MMA: the order of the
+// contraction does not matter as long as W and x agree, so a lane takes 8
+// channels in a row of two of W's rows and of one row of x, which are its
+// places in two MMAs of 16 channels. Bound by W's one pass: there is no
+// arithmetic to speak of (with products and sums on the ordinary pipes eight
+// rows took three times as long as one).
+template <int NT, typename T>
+__global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const FewRowsParams p) {
+  __shared__ float part[kFewWarps][NT][kFewColumns][8 + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int M = p.batches * p.rows, f0 = blockIdx.x * kFewColumns;
+  const T* const w0 = static_cast<const T*>(p.w) + (long long)(f0 + g) * p.w_stride;
+  const bool low = f0 + g + 8 < p.F;  // F is a multiple of 8: the upper eight rows are there, the lower may not be
+  const T* const w1 = low ? w0 + 8 * p.w_stride : w0;
+  const T* x[NT];
+  bool there[NT];
 #pragma unroll
-  for (int f = 0; f < FO; ++f)
+  for (int i = 0; i < NT; ++i) {
+    const int m = 8 * i + g;
+    there[i] = m < M;
+    x[i] = there[i] ? at<T>(p.x, m / p.rows, m % p.rows, 0) : static_cast<const T*>(p.x.data);
+  }
+  float acc[NT][4];
 #pragma unroll
-    for (int r = 0; r < R; ++r) acc[f][r] = 0;
-  const T* const w = static_cast<const T*>(p.w) + (long long)f0 * p.w_stride;
-  for (int k0 = 0; k0 < p.K; k0 += kSkinnyK) {
-    const int len = min(kSkinnyK, p.K - k0) / 8;
-    if (k0) __syncthreads();
-    for (int i = threadIdx.x; i < R * len; i += 256) {
-      const int r = i / len, c = i - r * len;
-      xs[r][c] = r < M ? *reinterpret_cast<const uint4*>(at<T>(p.x, r / p.rows, r % p.rows, k0 + c * 8)) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  const int steps = (p.K + 31) / 32, s0 = steps * warp / kFewWarps, s1 = steps * (warp + 1) / kFewWarps;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // the head that a step's channels lie in, kept up by additions
+  int head = p.x.heads > 1 ? s0 * 32 / p.x.D : 0;
+  int c = s0 * 32 - head * p.x.D + 8 * t;
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) {
+    const int k = s * 32 + 8 * t;
+    uint4 a0 = zero, a1 = zero, b[NT];
+    if (k < p.K) {
+      a0 = __ldg(reinterpret_cast<const uint4*>(w0 + k));
+      a1 = __ldg(reinterpret_cast<const uint4*>(w1 + k));
     }
-    __syncthreads();
-    if (f0 < p.F) {  // F is a multiple of 8: all columns lie inside
-#pragma unroll 2
-      for (int c = lane; c < len; c += 32) {
-        F2 a[FO][4];
 #pragma unroll
-        for (int f = 0; f < FO; ++f) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + f * p.w_stride + k0) + c);
-          a[f][0] = packed2<T>(q.x), a[f][1] = packed2<T>(q.y), a[f][2] = packed2<T>(q.z), a[f][3] = packed2<T>(q.w);
-        }
+    for (int i = 0; i < NT; ++i)
+      b[i] = there[i] && k < p.K ? *reinterpret_cast<const uint4*>(x[i] + head * p.x.s_h + c) : zero;
+    c += 32;
+    if (p.x.heads > 1 && c >= p.x.D) c -= p.x.D, ++head;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const uint4 q = xs[r][c];
-          const F2 x[4] = {packed2<T>(q.x), packed2<T>(q.y), packed2<T>(q.z), packed2<T>(q.w)};
-#pragma unroll
-          for (int f = 0; f < FO; ++f)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[f][r] = fma2(a[f][i], x[i], acc[f][r]);
-        }
-      }
+    for (int i = 0; i < NT; ++i) {
+      mma_16x8<T>(acc[i], a0.x, a1.x, a0.y, a1.y, b[i].x, b[i].y);
+      mma_16x8<T>(acc[i], a0.z, a1.z, a0.w, a1.w, b[i].z, b[i].w);
     }
   }
-  if (f0 >= p.F) return;
-  float mine = 0.f;
 #pragma unroll
-  for (int f = 0; f < FO; ++f)
+  for (int i = 0; i < NT; ++i) {
+    part[warp][i][g][2 * t] = acc[i][0];
+    part[warp][i][g][2 * t + 1] = acc[i][1];
+    part[warp][i][g + 8][2 * t] = acc[i][2];
+    part[warp][i][g + 8][2 * t + 1] = acc[i][3];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < NT * 8 * kFewColumns; e += 32 * kFewWarps) {
+    const int m = e / kFewColumns, f = e % kFewColumns, col = f0 + f;
+    if (m >= M || col >= p.F) continue;
+    float v[1] = {0.f};
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float2 h = split2(acc[f][r]);
-      float v = h.x + h.y;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == f * R + r) mine = v;
-    }
-  const int f = lane / R, r = lane % R;
-  if (f < FO && r < M) {
-    const int c = f0 + f, b = r / p.rows, n = r % p.rows;
-    if (p.bias) mine += p.bias[c];
-    if (p.z.data) *at<T>(p.z, b, n, c) = static_cast<T>(mine);
-    float one[1] = {mine};
-    activate_n(one, p.act);
-    mine = one[0];
-    if (p.residual.data) mine += static_cast<float>(*at<T>(p.residual, b, n, c));
-    *at<T>(p.out, b, n, c) = static_cast<T>(mine);
+    for (int i = 0; i < kFewWarps; ++i) v[0] += part[i][m / 8][f][m % 8];
+    const int batch = m / p.rows, n = m % p.rows;
+    if (p.bias) v[0] += p.bias[col];
+    if (p.z.data) *at<T>(p.z, batch, n, col) = static_cast<T>(v[0]);
+    activate_n(v, p.act);
+    if (p.residual.data) v[0] += static_cast<float>(*at<T>(p.residual, batch, n, col));
+    *at<T>(p.out, batch, n, col) = static_cast<T>(v[0]);
   }
 }
 
@@ -723,18 +742,13 @@ cudaError_t launch_gemm_kind(const GemmParams& p, int kind, int num_sms, cudaStr
   return launch_gemm<kGemmWeight, T>(p, num_sms, st);
 }
 
-template <int R, int FO, typename T>
-cudaError_t launch_skinny_rows(const SkinnyParams& p, cudaStream_t st) {
-  skinny_kernel<R, FO, T><<<(p.F + 8 * FO - 1) / (8 * FO), 256, 0, st>>>(p);
-  return cudaGetLastError();
-}
 template <typename T>
-cudaError_t launch_skinny(const SkinnyParams& p, cudaStream_t st) {
-  const int M = p.batches * p.rows;
-  if (M <= 1) return launch_skinny_rows<1, 2, T>(p, st);
-  if (M <= 2) return launch_skinny_rows<2, 2, T>(p, st);
-  if (M <= 4) return launch_skinny_rows<4, 2, T>(p, st);
-  return launch_skinny_rows<8, 4, T>(p, st);
+cudaError_t launch_few(const FewRowsParams& p, cudaStream_t st) {
+  const int M = p.batches * p.rows, blocks = (p.F + kFewColumns - 1) / kFewColumns, threads = 32 * kFewWarps;
+  if (M <= 8) few_rows_kernel<1, T><<<blocks, threads, 0, st>>>(p);
+  else if (M <= 16) few_rows_kernel<2, T><<<blocks, threads, 0, st>>>(p);
+  else few_rows_kernel<4, T><<<blocks, threads, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -749,8 +763,8 @@ cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t s
               : launch_behind(finish_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, p);
 }
 
-cudaError_t launch_linear_skinny(const SkinnyParams& p, int type, cudaStream_t st) {
-  return type ? launch_skinny<__half>(p, st) : launch_skinny<__nv_bfloat16>(p, st);
+cudaError_t launch_linear_few_rows(const FewRowsParams& p, int type, cudaStream_t st) {
+  return type ? launch_few<__half>(p, st) : launch_few<__nv_bfloat16>(p, st);
 }
 
 cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaStream_t st) {

@@ -208,6 +208,7 @@ struct GemmParams {
   float* partial;           // parts of split tiles [splits, rest, 256, bn]
   int wide;                 // out, residual, z and partial are accessed in aligned 32-byte pieces
   int a_d, b_d;             // channels of a head of A, B
+  int a_rows;               // rows of A's boxes (K-major)
   int bn;                   // columns of a tile: a multiple of 32, 64 to 256
   int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
   int rows;                 // rows of a batch
@@ -231,7 +232,7 @@ struct FinishParams {
   RowsView residual, z, out;   // data null: none
 };
 
-struct SkinnyParams {
+struct FewRowsParams {
   RowsView x, residual, z, out;
   const void* w;
   long long w_stride;
@@ -249,11 +250,11 @@ struct SlopeParams {
 };
 
 enum : int { kGemmForward = 0, kGemmInput = 1, kGemmWeight = 2 };
-constexpr int kSkinnyRows = 8;
+constexpr int kFewRows = 16;
 // type: 0 bf16, 1 fp16
 cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_sms, cudaStream_t st);
 cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t st);
-cudaError_t launch_linear_skinny(const SkinnyParams& p, int type, cudaStream_t st);
+cudaError_t launch_linear_few_rows(const FewRowsParams& p, int type, cudaStream_t st);
 cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaStream_t st);
 // Reads and clears the current device's error word of the linear kernels (synchronises the stream).
 cudaError_t linear_error_word(int* word, cudaStream_t st);
