@@ -12,7 +12,7 @@ using vsa::RowsView;
 std::atomic<unsigned long long> g_wait_ns{1000000000ull};
 std::atomic<int> g_stall{0};
 
-inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+inline size_t align_up(size_t x, size_t to = 256) { return (x + to - 1) / to * to; }
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // How a product of `batches` x `rows` x `cols` over `kblocks` 64-long steps is
@@ -22,10 +22,11 @@ struct Tiling {
   long long whole, rest;
 };
 
-// The pairs of CTAs run in rounds; a round costs its steps (the MMA of a step
-// takes 2 bn cycles, its loads 16 + bn/16 KB at the 47 bytes a cycle that an
-// SM gets of the L2's rate) plus the start of a tile, and at the end there is
-// an epilogue. The last round's tiles are too few for all pairs and are split
+// The pairs of CTAs run in rounds. A step of a round costs the MMA's 2 bn
+// cycles, or its loads (16 KB of A, less with few rows, and bn/16 KB, at the 47
+// bytes a cycle that an SM gets of the L2's rate), or their issue; a round its
+// steps or the epilogue of the tile before (20 cycles a column), and the start
+// of a tile. The last round's tiles are too few for all pairs and are split
 // along the contraction, which costs a second kernel that reads the parts.
 // `wide` allows only tiles whose second half of columns does not start inside
 // a head.
@@ -37,8 +38,11 @@ Tiling choose(long long batches, long long rows, long long cols, long long kbloc
     if (wide && bn % 128) continue;
     const long long tiles = batches * ceil_div(rows, 256) * ceil_div(cols, bn), whole = tiles / pairs * pairs;
     const long long rest = tiles - whole;
-    const double load = (16384 + 64.0 * bn) / 47, step = load > 2.0 * bn ? load : 2.0 * bn;
-    const double base = whole / pairs * (kblocks * step + 800) + 12.0 * bn;
+    double step = (128.0 * (rows < 128 ? rows : 128) + 64.0 * bn) / 47;
+    for (double least : {2.0 * bn, 140.0})
+      if (step < least) step = least;
+    const double epilogue = 20.0 * bn, all = kblocks * step;
+    const double base = whole / pairs * ((all > epilogue ? all : epilogue) + 800) + epilogue;
     const long long fill = rest ? pairs / rest : 1;  // parts that give every pair one
     for (long long s : {1LL, fill / 2, fill}) {
       if (s > 32) s = 32;
@@ -186,6 +190,12 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   const int half = p.t.bn / 2;
   g.a_rows = p.rows < 128 ? (int)ceil_div(p.rows, 8) * 8 : 128;
   vsa_status e = encode(&g.ta, a, run_rows, runs, weight ? 64 : g.a_rows, type);
+  // Few rows make a small tile of A: the MMAs then read what lies behind it,
+  // other operands inside the ring, for rows that are not stored.
+  g.tile_a = weight ? 16384 : g.a_rows * 128;
+  g.stage_bytes = g.tile_a + (p.kind == vsa::kGemmForward ? (int)align_up(half * 128, 1024) : (half + 63) / 64 * 8192);
+  g.stages = (7 * 32768 - (16384 - g.tile_a)) / g.stage_bytes;
+  if (g.stages > vsa::kGemmMaxStages) g.stages = vsa::kGemmMaxStages;
   if (e == VSA_OK) e = encode(&g.tb, b, b_rows, weight ? runs : 1, p.kind == vsa::kGemmForward ? half : 64, type);
   if (e != VSA_OK) return e;
   g.out = ep.out;

@@ -12,9 +12,9 @@
 //    each CTA holds 128 rows of A and half of B's rows, tcgen05.mma
 //    (cta_group::2) reads both halves, so a CTA loads 16 + bn/16 KB a 64-long
 //    step of the contraction instead of the 16 + bn/8 KB of a lone CTA: the
-//    L2 -> SM rate, not the tensor cores, would bound the latter. One thread
-//    issues the loads (7 stages of 32 KB), one the MMAs, eight warps the
-//    epilogue of the tile before (two accumulators of up to 256 columns fill
+//    L2 -> SM rate, not the tensor cores, would bound the latter. Two warps
+//    issue the loads (7 stages of 32 KB, or more and smaller ones), one the
+//    MMAs, eight the epilogue of the tile before (two accumulators of up to 256 columns fill
 //    the SM's tensor memory). Bound by the tensor cores where the product is
 //    large.
 //  * finish_kernel joins the parts of a contraction that was split because it
@@ -42,17 +42,17 @@ using namespace ptx;
 
 __device__ int g_linear_error;
 
-constexpr int kStages = 7, kStageBytes = 32768, kTileA = 16384;
-constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kRingBytes = 7 * 32768, kTileA = 16384;
+constexpr int kEpiWarps = 8, kThreads = 96 + 32 * kEpiWarps;  // two warps load, one issues MMAs
 constexpr int kAccColumns = 256;
 
 struct Barriers {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kGemmMaxStages], empty[kGemmMaxStages];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drained;
   uint32_t tmem;
 };
-constexpr int kGemmSmem = 1024 + kStages * kStageBytes + (int)sizeof(Barriers);
+constexpr int kGemmSmem = 1024 + kRingBytes + (int)sizeof(Barriers);
 static_assert(kGemmSmem <= 227 * 1024, "shared memory");
 
 // ---------------------------------------------------------------- arithmetic
@@ -301,10 +301,11 @@ struct Unit {
 
 // Stage of the ring and the parity of its use.
 struct Ring {
-  int stage = 0;
+  int stage = 0, stages;
   uint32_t parity = 0;
+  __device__ __forceinline__ explicit Ring(const GemmParams& p) : stages(p.stages) {}
   __device__ __forceinline__ void next() {
-    if (++stage == kStages) stage = 0, parity ^= 1;
+    if (++stage == stages) stage = 0, parity ^= 1;
   }
 };
 
@@ -314,7 +315,7 @@ template <int KIND, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  Barriers& sh = *reinterpret_cast<Barriers*>(raw + (base - smem_u32(raw)) + kStages * kStageBytes);
+  Barriers& sh = *reinterpret_cast<Barriers*>(raw + (base - smem_u32(raw)) + kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = (unsigned)p.units;
@@ -322,14 +323,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   const Waiter wait{p.wait_ns};
 
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
+    for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     prefetch_tmap(&p.ta);
     prefetch_tmap(&p.tb);
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tmem_alloc_pair(&sh.tmem, 512);
     tmem_relinquish_pair();
   }
@@ -341,16 +342,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   ptx::wait_for_previous();
   ptx::let_next_start();
 
-  // The two issuing warps run their loops as whole warps, so that what they
+  // The issuing warps run their loops as whole warps, so that what they
   // compute is uniform, and elect a lane to issue.
-  if (warp == 0) {
-    // ---- loads of this CTA's operand rows; both CTAs' complete on the even CTA's barriers
+  if (warp < 2) {
+    // ---- loads of this CTA's operand rows; both CTAs' complete on the even
+    // CTA's barriers. The two warps take every second step.
     const int b_boxes = (half + 63) / 64;
     const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : b_boxes * 8192;
     const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
     const bool load = p.stall == 0;
-    Ring ring;
-    bool ok = true;
+    Ring ring(p);
+    bool ok = true, mine = warp == 0;
     for (unsigned u = pair; ok && u < units; u += pairs) {
       // Divisions here; the steps keep their coordinates up by additions (a
       // division costs the issuing warp more than a load).
@@ -380,11 +382,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       const uint32_t pair_bytes = 2 * b_bytes + (KIND == kGemmWeight || w.row0 + 128 < p.rows ? 2 : 1) * a_bytes;
       for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
         const int s = ring.stage;
-        ok = wait.warp(&sh.empty[s], ring.parity ^ 1);  // passes at once where no use came before
-        if (!ok) break;
-        if (elect_one()) {
+        // passes at once where no use came before
+        if (mine && !(ok = wait.warp(&sh.empty[s], ring.parity ^ 1))) break;
+        if (mine && elect_one()) {
           const uint32_t bar = full0 + s * 8;
-          const uint32_t a = base + s * kStageBytes, b = a + kTileA;
+          const uint32_t a = base + s * p.stage_bytes, b = a + p.tile_a;
           if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], pair_bytes);
           if (load) {
             if (KIND == kGemmWeight) {
@@ -403,22 +405,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
             }
           }
         }
+        mine = !mine;
         k += 64;
         if (k >= kend) k = 0, ++kh;
       }
     }
     if (!ok && rank == 0)  // the loads in flight land before the pair's shared memory goes
-      for (int i = 0; i < kStages; ++i)
+      for (int i = 0; i < p.stages; ++i)
         mbar_wait(&sh.full[i], i < ring.stage ? ring.parity : ring.parity ^ 1, p.wait_ns);
-  } else if (warp == 1) {
+  } else if (warp == 2) {
     if (rank == 0) {
       // ---- MMAs of the pair
       const uint32_t idesc =
           idesc_f16_f32(256, p.bn, KIND == kGemmWeight, KIND != kGemmForward, std::is_same<T, __nv_bfloat16>::value);
       constexpr uint32_t A_STEP = (KIND == kGemmWeight ? 2048 : 32) >> 4, B_STEP = (KIND == kGemmForward ? 32 : 2048) >> 4;
       const uint64_t ad0 = sdesc_sw128(base, KIND == kGemmWeight ? 8192 : 16, 1024);
-      const uint64_t bd0 = sdesc_sw128(base + kTileA, KIND == kGemmForward ? 16 : 8192, 1024);
-      Ring ring;
+      const uint64_t bd0 = sdesc_sw128(base + p.tile_a, KIND == kGemmForward ? 16 : 8192, 1024);
+      Ring ring(p);
       int tile = 0;
       bool ok = true;
       for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
@@ -436,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ad = ad0 + (uint64_t)(s * (kStageBytes >> 4)), bd = bd0 + (uint64_t)(s * (kStageBytes >> 4));
+            const uint64_t at = (uint64_t)(s * (p.stage_bytes >> 4)), ad = ad0 + at, bd = bd0 + at;
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_f16_ss_pair(acc, ad + i * A_STEP, bd + i * B_STEP, idesc, i ? 1u : add);
             mma_commit_pair(&sh.empty[s]);
@@ -456,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     // in whole 32-byte sectors. Shared memory has no bandwidth to spare: the
     // MMAs read 64 bytes a cycle of it and the loads write as many (%STG%).
     const int quarter = warp & 3, groups = p.bn / 32;
-    const int g0 = warp < 6 ? 0 : (groups + 1) / 2, g1 = warp < 6 ? (groups + 1) / 2 : groups;
+    const int g0 = warp < 7 ? 0 : (groups + 1) / 2, g1 = warp < 7 ? (groups + 1) / 2 : groups;
     int tile = 0;
     for (unsigned u = pair; u < units; u += pairs, ++tile) {
       const Unit w(p, u);
@@ -529,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 2) tmem_dealloc_pair(tmem, 512);
 }
 
 // ---------------------------------------------------------------- split contractions
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
 }
 
 // ---------------------------------------------------------------- few rows
-constexpr int kFewWarps = 8, kFewColumns = 16;
+constexpr int kFewWarps = 16, kFewColumns = 16;
 
 // D += A B with A [16 x 16] (W's rows), B [16 x 8] (x's rows as columns).
 template <typename T>

@@ -209,6 +209,8 @@ struct GemmParams {
   int wide;                 // out, residual, z and partial are accessed in aligned 32-byte pieces
   int a_d, b_d;             // channels of a head of A, B
   int a_rows;               // rows of A's boxes (K-major)
+  int stages, stage_bytes;  // ring of operand stages: A's tile, then B's at tile_a
+  int tile_a;
   int bn;                   // columns of a tile: a multiple of 32, 64 to 256
   int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
   int rows;                 // rows of a batch
@@ -251,6 +253,7 @@ struct SlopeParams {
 
 enum : int { kGemmForward = 0, kGemmInput = 1, kGemmWeight = 2 };
 constexpr int kFewRows = 16;
+constexpr int kGemmMaxStages = 16;
 // type: 0 bf16, 1 fp16
 cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_sms, cudaStream_t st);
 cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t st);
