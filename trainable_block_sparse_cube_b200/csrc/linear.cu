@@ -247,8 +247,9 @@ __device__ __forceinline__ T* at(const RowsView& v, int b, int n, int c) {
 // Bounded waits; a warp's lanes give up together.
 struct Waiter {
   unsigned long long limit;
-  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)) || gave_up();
+  // `seen`: what an earlier look at the barrier found.
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, bool seen = false) const {
+    return __all_sync(0xffffffffu, seen) || __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)) || gave_up();
   }
   __device__ __forceinline__ bool pair(uint64_t* bar, uint32_t parity) const {  // arrivals of both CTAs
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit)) || gave_up();
@@ -307,6 +308,11 @@ struct Ring {
   __device__ __forceinline__ void next() {
     if (++stage == stages) stage = 0, parity ^= 1;
   }
+  __device__ __forceinline__ Ring after(int n) const {
+    Ring r = *this;
+    for (int i = 0; i < n; ++i) r.next();
+    return r;
+  }
 };
 
 // KIND kGemmForward: A and B K-major. kGemmInput: A K-major, B MN-major.
@@ -352,7 +358,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
     const bool load = p.stall == 0;
     Ring ring(p);
-    bool ok = true, mine = warp == 0;
+    // A look at the next barrier is taken before this step's work: its answer
+    // is there when it is needed.
+    bool ok = true, mine = warp == 0, seen = true;
     for (unsigned u = pair; ok && u < units; u += pairs) {
       // Divisions here; the steps keep their coordinates up by additions (a
       // division costs the issuing warp more than a load).
@@ -383,7 +391,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
         const int s = ring.stage;
         // passes at once where no use came before
-        if (mine && !(ok = wait.warp(&sh.empty[s], ring.parity ^ 1))) break;
+        if (mine) {
+          if (!(ok = wait.warp(&sh.empty[s], ring.parity ^ 1, seen))) break;
+          const Ring next = ring.after(2);
+          seen = mbar_test(&sh.empty[next.stage], next.parity ^ 1);
+        }
         if (mine && elect_one()) {
           const uint32_t bar = full0 + s * 8;
           const uint32_t a = base + s * p.stage_bytes, b = a + p.tile_a;
@@ -423,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       const uint64_t bd0 = sdesc_sw128(base + p.tile_a, KIND == kGemmForward ? 16 : 8192, 1024);
       Ring ring(p);
       int tile = 0;
-      bool ok = true;
+      bool ok = true, seen = false;
       for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
         int k0, k1;
         Unit::steps(p, u, &k0, &k1);
@@ -435,9 +447,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
         uint32_t add = 0;
         for (int kb = k0; kb < k1; ++kb, ring.next()) {
           const int s = ring.stage;
-          ok = wait.warp(&sh.full[s], ring.parity);
+          ok = wait.warp(&sh.full[s], ring.parity, seen);
           if (!ok) break;
           tc_fence_after();
+          const Ring next = ring.after(1);
+          seen = mbar_test(&sh.full[next.stage], next.parity);
           if (elect_one()) {
             const uint64_t at = (uint64_t)(s * (p.stage_bytes >> 4)), ad = ad0 + at, bd = bd0 + at;
 #pragma unroll
