@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
 }
 
 // ---------------------------------------------------------------- few rows
-constexpr int kFewWarps = 16, kFewColumns = 16;
+constexpr int kFewColumns = 16;
 
 // D += A B with A [16 x 16] (W's rows), B [16 x 8] (x's rows as columns).
 template <typename T>
@@ -610,9 +610,10 @@ __device__ __forceinline__ void mma_16x8(float (&d)[4], uint32_t a0, uint32_t a1
 // places in two MMAs of 16 channels. Bound by W's one pass: there is no
 // arithmetic to speak of (with products and sums on the ordinary pipes eight
 // rows took three times as long as one).
-template <int NT, typename T>
-__global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const FewRowsParams p) {
-  __shared__ float part[kFewWarps][NT][kFewColumns][8 + 1];
+template <int NT, int WARPS, typename T>
+__global__ void __launch_bounds__(32 * WARPS) few_rows_kernel(const FewRowsParams p) {
+  constexpr int UNROLL = NT > 2 ? 2 : 4;
+  __shared__ float part[WARPS][NT][kFewColumns][8 + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int M = p.batches * p.rows, f0 = blockIdx.x * kFewColumns;
   const T* const w0 = static_cast<const T*>(p.w) + (long long)(f0 + g) * p.w_stride;
@@ -629,12 +630,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const FewRowsP
   float acc[NT][4];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  const int steps = (p.K + 31) / 32, s0 = steps * warp / kFewWarps, s1 = steps * (warp + 1) / kFewWarps;
+  const int steps = (p.K + 31) / 32, s0 = steps * warp / WARPS, s1 = steps * (warp + 1) / WARPS;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // the head that a step's channels lie in, kept up by additions
   int head = p.x.heads > 1 ? s0 * 32 / p.x.D : 0;
   int c = s0 * 32 - head * p.x.D + 8 * t;
-#pragma unroll 4
+#pragma unroll UNROLL
   for (int s = s0; s < s1; ++s) {
     const int k = s * 32 + 8 * t;
     uint4 a0 = zero, a1 = zero, b[NT];
@@ -661,12 +662,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const FewRowsP
     part[warp][i][g + 8][2 * t + 1] = acc[i][3];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < NT * 8 * kFewColumns; e += 32 * kFewWarps) {
+  for (int e = threadIdx.x; e < NT * 8 * kFewColumns; e += 32 * WARPS) {
     const int m = e / kFewColumns, f = e % kFewColumns, col = f0 + f;
     if (m >= M || col >= p.F) continue;
     float v[1] = {0.f};
 #pragma unroll
-    for (int i = 0; i < kFewWarps; ++i) v[0] += part[i][m / 8][f][m % 8];
+    for (int i = 0; i < WARPS; ++i) v[0] += part[i][m / 8][f][m % 8];
     const int batch = m / p.rows, n = m % p.rows;
     if (p.bias) v[0] += p.bias[col];
     if (p.z.data) *at<T>(p.z, batch, n, col) = static_cast<T>(v[0]);
@@ -759,13 +760,22 @@ cudaError_t launch_gemm_kind(const GemmParams& p, int kind, int num_sms, cudaStr
   return launch_gemm<kGemmWeight, T>(p, num_sms, st);
 }
 
+// Long rows take sixteen warps a block, which keeps more of W in flight; for
+// short ones the joining of the warps' sums would cost more (one row: 1536 x
+// 9216 7.2 us with eight and 8.8 with sixteen, 4096 x 4096 11.4 and 8.7).
+template <int NT, typename T>
+cudaError_t launch_few_tiles(const FewRowsParams& p, cudaStream_t st) {
+  const int blocks = (p.F + kFewColumns - 1) / kFewColumns;
+  if (p.K > 2048) few_rows_kernel<NT, 16, T><<<blocks, 512, 0, st>>>(p);
+  else few_rows_kernel<NT, 8, T><<<blocks, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t launch_few(const FewRowsParams& p, cudaStream_t st) {
-  const int M = p.batches * p.rows, blocks = (p.F + kFewColumns - 1) / kFewColumns, threads = 32 * kFewWarps;
-  if (M <= 8) few_rows_kernel<1, T><<<blocks, threads, 0, st>>>(p);
-  else if (M <= 16) few_rows_kernel<2, T><<<blocks, threads, 0, st>>>(p);
-  else few_rows_kernel<4, T><<<blocks, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  const int M = p.batches * p.rows;
+  if (M <= 8) return launch_few_tiles<1, T>(p, st);
+  if (M <= 16) return launch_few_tiles<2, T>(p, st);
+  return launch_few_tiles<4, T>(p, st);
 }
 
 }  // namespace

@@ -252,7 +252,7 @@ struct SlopeParams {
 };
 
 enum : int { kGemmForward = 0, kGemmInput = 1, kGemmWeight = 2 };
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 32;
 constexpr int kGemmMaxStages = 16;
 // type: 0 bf16, 1 fp16
 cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_sms, cudaStream_t st);
