@@ -22,37 +22,43 @@ struct Tiling {
   long long whole, rest;
 };
 
-// The pairs of CTAs run in rounds. A step of a round costs the MMA's 2 bn
-// cycles, or its loads (16 KB of A, less with few rows, and bn/16 KB, at the 47
-// bytes a cycle that an SM gets of the L2's rate), or their issue; a round its
-// steps or the epilogue of the tile before (20 cycles a column), and the start
-// of a tile. The last round's tiles are too few for all pairs and are split
-// along the contraction, which costs a second kernel that reads the parts.
+// The pairs of CTAs run in rounds; costs in cycles, measured at one tile a pair
+// (64 steps of 256 x bn, ns a step: bn 64 205, 128 217, 192 395, 256 506, where
+// B comes from memory). A step costs the most of
+//   its MMA, 2 bn;
+//   its loads, 16 KB of A (less with few rows) and bn/16 KB of B, at the 47
+//   bytes a cycle that an SM gets of the L2's rate;
+//   B's way from memory, at 3400 bytes a cycle for all pairs, those above one
+//   another sharing it;
+//   400, the issue of a step.
+// A round costs its steps, or the epilogue of the tile before, and the start of
+// a tile. The last round's tiles are too few for all pairs and are split along
+// the contraction, which costs a second kernel that reads the parts (40 x 4096
+// x 4096: 64 tiles of 64 columns 17.3 us, 22 of 192 in three parts 13.8).
 // `wide` allows only tiles whose second half of columns does not start inside
 // a head.
 Tiling choose(long long batches, long long rows, long long cols, long long kblocks, int sms, bool wide) {
-  const long long pairs = sms / 2;
+  const long long pairs = sms / 2, row_tiles = batches * ceil_div(rows, 256);
+  const double tile_rows = rows < 256 ? rows : 256;
   Tiling best{};
   double best_cost = -1;
   for (int bn = 256; bn >= 64; bn -= 32) {
     if (wide && bn % 128) continue;
-    const long long tiles = batches * ceil_div(rows, 256) * ceil_div(cols, bn), whole = tiles / pairs * pairs;
-    const long long rest = tiles - whole;
-    double step = (128.0 * (rows < 128 ? rows : 128) + 64.0 * bn) / 47;
-    for (double least : {2.0 * bn, 140.0})
-      if (step < least) step = least;
-    const double epilogue = 20.0 * bn, all = kblocks * step;
+    const long long tiles = row_tiles * ceil_div(cols, bn), whole = tiles / pairs * pairs, rest = tiles - whole;
+    const double least[] = {2.0 * bn, (128.0 * (tile_rows < 128 ? tile_rows : 128) + 64.0 * bn) / 47,
+                            128.0 * bn * (tiles < pairs ? tiles : pairs) / (row_tiles < 8 ? row_tiles : 8) / 3400};
+    double step = 400;
+    for (double c : least)
+      if (step < c) step = c;
+    const double epilogue = 2000 + 25.0 * bn, all = kblocks * step;
     const double base = whole / pairs * ((all > epilogue ? all : epilogue) + 800) + epilogue;
-    const long long fill = rest ? pairs / rest : 1;  // parts that give every pair one
-    for (long long s : {1LL, fill / 2, fill}) {
-      if (s > 32) s = 32;
-      if (s > kblocks) s = kblocks;
-      if (s < 1) continue;
-      double cost = base + ceil_div(rest * s, pairs) * (ceil_div(kblocks, s) * step + 800);
-      if (s > 1) cost += 5000 + 8.0 * s * rest * 256 * bn / 2700;
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (s > 1 && (s > kblocks || rest * s > pairs || !rest)) break;
+      double cost = base + (rest ? ceil_div(kblocks, s) * step + 800 : 0);
+      if (s > 1) cost += 2500 + 8.0 * s * rest * tile_rows * bn / 2700;
       if (best_cost < 0 || cost < best_cost) {
         best_cost = cost;
-        best = s > 1 ? Tiling{bn, (int)s, whole, rest} : Tiling{bn, 1, tiles, 0};
+        best = s > 1 ? Tiling{bn, s, whole, rest} : Tiling{bn, 1, tiles, 0};
       }
     }
   }
