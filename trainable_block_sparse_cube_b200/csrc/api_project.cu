@@ -30,7 +30,7 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
   for (int j = 0; j < r->rot / 2; ++j) {
     if (r->axis[j] < 0 || r->axis[j] >= r->axes || !std::isfinite(r->freq[j])) return VSA_ERR_INVALID_ARG;
     p->axis[j] = r->axis[j];
-    p->freq[j] = r->freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
+    p->freq[j] = r->freq[j] * 0.63661977236758134308;  // 2 / pi
   }
   if (!o->list) {
     if (r->axes != 3 || o->T < 1 || o->H < 1 || o->W < 1) return VSA_ERR_SHAPE;

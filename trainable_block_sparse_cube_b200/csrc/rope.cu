@@ -10,9 +10,9 @@
 //
 // r is recomputed from x, which the backward reads anyway, so nothing is
 // saved. Everything between the loads and the stores is fp32 and rounded
-// once; the angles are formed in fp64 as turns (p f / 2 pi), reduced to
-// [-1/2, 1/2] there, and only then handed to the fp32 sine and cosine:
-// a position of 10^6 would otherwise cost the angle 20 of its 24 bits.
+// once; the angles are formed in fp64 as quarter turns (2 p f / pi), reduced to
+// [-1/2, 1/2] there, and only then turned into fp32 sine and cosine: a
+// position of 10^6 would otherwise cost the angle 20 of its 24 bits.
 //
 // Bound by HBM: a row is read once and written once (the norm's backward
 // reads x and dy). A lane moves 8 channels, a power of two of lanes a row, and
@@ -181,27 +181,43 @@ struct Place {
         }
       }
     } else {
-      const int first = (chunk * 8) % (rot > 0 ? rot / 2 : 1);
+      // the two chunks of a pair of halves need the same eight angles: each computes four
+      const int first = (chunk * 8) % (rot > 0 ? rot / 2 : 1) + (sign < 0.f ? 0 : 4);
+      float cs[4], sn[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-        if (turned) {
-          float sn, cs;
-          turn(freq, axis, pos, first + i, &sn, &cs);
-          c[i] = cs;
-          s[i] = sign * dir * sn;
-        }
+      for (int i = 0; i < 4; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+        if (turned) turn(freq, axis, pos, first + i, &sn[i], &cs[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float oc = __shfl_sync(0xffffffffu, cs[i], partner), os = __shfl_sync(0xffffffffu, sn[i], partner);
+        c[i] = sign < 0.f ? cs[i] : oc;
+        s[i] = sign * dir * (sign < 0.f ? sn[i] : os);
+        c[i + 4] = sign < 0.f ? oc : cs[i];
+        s[i + 4] = sign * dir * (sign < 0.f ? os : sn[i]);
       }
     }
   }
 
+  // Sine and cosine of p freq quarter turns. The nearest whole number of them is
+  // taken off in fp64 (adding 1.5 x 2^52 leaves it in the low bits), and what
+  // is left, at most an eighth of a turn, goes into the Taylor polynomials
+  // (to x^9 and x^8: 2e-9 and 3e-8 at the ends).
   __device__ __forceinline__ static void turn(const double* freq, const int* axis, const double (&pos)[kRopeAxes],
                                               int j, float* sn, float* cs) {
+    constexpr double kWhole = 6755399441055744.0;
     const int a = axis[j];
     const double p = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-    const double turns = p * freq[j];
-    sincospif(2.f * (float)(turns - rint(turns)), sn, cs);
+    const double q = p * freq[j], near = q + kWhole;
+    const float x = (float)(q - (near - kWhole)) * 1.57079632679489662f, x2 = x * x;
+    const int quarter = __double2loint(near);
+    const float sine = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+    const float cosine = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+    const float u = quarter & 1 ? cosine : sine, v = quarter & 1 ? sine : cosine;
+    *sn = quarter & 2 ? -u : u;
+    *cs = (quarter + 1) & 2 ? -v : v;
   }
 
   // The other channel of each pair (0 where a channel is not rotated, so that
@@ -248,7 +264,7 @@ __device__ __forceinline__ void token_positions(const RopeParams& p, int b, int 
   }
 }
 
-// Frequencies (in turns) and axes from the launch parameters to shared memory.
+// Frequencies (in quarter turns) and axes from the launch parameters to shared memory.
 __device__ __forceinline__ void stage_rotation(const RopeParams& p, double* freq, int* axis) {
   for (int j = threadIdx.x; j < p.rot / 2; j += kThreads) {
     freq[j] = p.freq[j];

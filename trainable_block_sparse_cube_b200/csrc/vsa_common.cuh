@@ -171,7 +171,7 @@ struct RopeParams {
   int B, N, D;
   int rot, interleaved;     // rotated leading channels; pairs (2i, 2i + 1) or (i, i + rot/2)
   int axes;
-  double freq[kRopePairs];  // turns (radians / 2 pi) per unit of position
+  double freq[kRopePairs];  // quarter turns (radians x 2 / pi) per unit of position
   int axis[kRopePairs];
   int pos_kind;             // 0: raster grid of H x W frames; 1: int32 list; 2: fp32 list
   int H, W, origin[3];
