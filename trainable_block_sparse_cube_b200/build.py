@@ -30,7 +30,7 @@ def _nvcc() -> str:
 def build(verbose: bool = False, force: bool = False) -> str:
     srcs = [os.path.join(HERE, "csrc", s) for s in SRC]
     deps = srcs + [os.path.join(HERE, "csrc", h) for h in ("vsa_common.cuh", "sm100_ptx.cuh", "pair_ptx.cuh", "host.cuh",
-                                                            "packed.cuh", "behind.cuh")]
+                                                            "packed.cuh", "launch.cuh")]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "vsa.h"))
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)

@@ -27,11 +27,10 @@
 // the unrounded values.
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "pair_ptx.cuh"
-#include "behind.cuh"
 #include "vsa_common.cuh"
 
 namespace vsa {
@@ -739,16 +738,8 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* partial, 
 
 template <int KIND, typename T>
 cudaError_t launch_gemm(const GemmParams& p, int num_sms, cudaStream_t st) {
-  constexpr int kMaxDevices = 64;
-  static std::atomic<bool> ready[kMaxDevices];  // the attribute belongs to the device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem<gemm_kernel<KIND, T>>(kGemmSmem);
   if (e != cudaSuccess) return e;
-  if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(gemm_kernel<KIND, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
-  }
   const long long pairs = p.units < num_sms / 2 ? p.units : num_sms / 2;
   return launch_behind(gemm_kernel<KIND, T>, dim3((unsigned)(2 * pairs)), dim3(kThreads), kGemmSmem, st, p);
 }

@@ -30,7 +30,7 @@
 // order: no atomics, the same bits every time.
 #include <cuda_fp16.h>
 
-#include "behind.cuh"
+#include "launch.cuh"
 #include "packed.cuh"
 #include "sm100_ptx.cuh"
 #include "vsa_common.cuh"
@@ -40,6 +40,7 @@ namespace vsa {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kBackwardStages = 4;
 constexpr int kForwardPerSm = 4, kBackwardPerSm = 3;      // blocks of an SM
 constexpr int kForwardAngles = 5, kBackwardAngles = 3;    // rows whose work an angle's equals, see plan_units
 
@@ -474,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
 // block's weight gradients to p.partial[block][tensor][D].
 template <typename T, int L, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int STAGES = sizeof(T) == 4 ? 2 : 4;
+  constexpr int STAGES = kBackwardStages;
+  extern __shared__ uint4 ring[];
   __shared__ double freq[kRopePairs];
   __shared__ int axis[kRopePairs];
   __shared__ float part[2][8][kThreads];  // a thread's sums of 8 channels over its rows so far
-  __shared__ uint4 ring[STAGES][Feed<T, 2, true, STAGES>::SLOTS][kThreads];
   constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
@@ -614,8 +615,12 @@ int plan_units(RopeParams& p, int num_sms, int per_sm, int angles) {
 template <typename T, int L, bool INTER>
 cudaError_t launch_typed(const RopeParams& p, bool backward, int grid, cudaStream_t st) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;
-  if (backward) norm_rope_backward_kernel<T, L, INTER><<<grid, kThreads, 0, st>>>(p);
-  else rope_kernel<T, L, INTER, U><<<grid, kThreads, 0, st>>>(p);
+  if (backward) {
+    constexpr int smem = Feed<T, 2, true, kBackwardStages>::END;
+    const cudaError_t e = allow_smem<norm_rope_backward_kernel<T, L, INTER>>(smem);
+    if (e != cudaSuccess) return e;
+    norm_rope_backward_kernel<T, L, INTER><<<grid, kThreads, smem, st>>>(p);
+  } else rope_kernel<T, L, INTER, U><<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
