@@ -29,8 +29,11 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
   p->axes = r->axes;
   for (int j = 0; j < r->rot / 2; ++j) {
     if (r->axis[j] < 0 || r->axis[j] >= r->axes || !std::isfinite(r->freq[j])) return VSA_ERR_INVALID_ARG;
-    p->axis[j] = r->axis[j];
-    p->freq[j] = r->freq[j] * 0.63661977236758134308;  // 2 / pi
+    const double turns = r->freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double whole = std::floor(turns), fraction = turns - whole;
+    const uint64_t bits = fraction < 1.0 ? (uint64_t)(fraction * 18446744073709551616.0) : 0;  // 2^64
+    const double around = whole - 4294967296.0 * std::floor(whole / 4294967296.0);             // modulo 2^32
+    p->pairs[j] = vsa::RopePair{(uint32_t)bits, (uint32_t)(bits >> 32), (uint32_t)(uint64_t)around, r->axis[j]};
   }
   if (!o->list) {
     if (r->axes != 3 || o->T < 1 || o->H < 1 || o->W < 1) return VSA_ERR_SHAPE;
@@ -40,6 +43,8 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
     p->pos_kind = 0;
     p->H = o->H;
     p->W = o->W;
+    p->by_h = vsa::Divisor(o->H);
+    p->by_w = vsa::Divisor(o->W);
     for (int a = 0; a < 3; ++a) p->origin[a] = o->origin[a];
   } else {
     if (o->list_type != 0 && o->list_type != 1) return VSA_ERR_UNSUPPORTED;

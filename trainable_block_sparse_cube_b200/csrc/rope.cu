@@ -10,9 +10,11 @@
 //
 // r is recomputed from x, which the backward reads anyway, so nothing is
 // saved. Everything between the loads and the stores is fp32 and rounded
-// once; the angles are formed in fp64 as quarter turns (2 p f / pi), reduced to
-// [-1/2, 1/2] there, and only then turned into fp32 sine and cosine: a
-// position of 10^6 would otherwise cost the angle 20 of its 24 bits.
+// once. A whole position times the fraction of a turn that a pair makes for one,
+// in 64 bits, keeps just the fraction of a turn in the low 64 bits of the
+// product: exact to 2^-32 of a turn for any position, where fp32 would have
+// lost 20 of its 24 bits at 10^6. The rest of an fp32 position adds its own
+// product.
 //
 // Bound by HBM: a row is read once and written once (the norm's backward
 // reads x and dy). A lane moves 8 channels, a power of two of lanes a row, and
@@ -42,7 +44,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kBackwardStages = 4;
 constexpr int kForwardPerSm = 4, kBackwardPerSm = 3;      // blocks of an SM
-constexpr int kForwardAngles = 5, kBackwardAngles = 3;    // rows whose work an angle's equals, see plan_units
+constexpr int kForwardAngles = 3, kBackwardAngles = 2;    // rows whose work an angle's equals, see plan_units
 
 template <typename T>
 struct Row8;  // 8 channels as they lie in memory
@@ -138,6 +140,68 @@ __device__ __forceinline__ void row_sums(F2 (&v)[N]) {
   }
 }
 
+// A token's positions: the whole part as 32 low bits and what is above them,
+// and, of an fp32 one, the rest in 2^-32.
+struct Positions {
+  uint32_t low[kRopeAxes], rest[kRopeAxes];
+  int high[kRopeAxes];
+  float bad[kRopeAxes];  // NaN for a position that is not finite, else 0
+
+  __device__ __forceinline__ void whole(int a, long long v) {
+    low[a] = (uint32_t)v;
+    high[a] = (int)(v >> 32);
+  }
+  __device__ __forceinline__ Positions(const RopeParams& p, int b, int n) {
+    if (p.pos_kind == 0) {  // the raster grid's (t, h, w)
+      const unsigned th = p.by_w(n), t = p.by_h(th);
+      whole(0, (long long)t + p.origin[0]);
+      whole(1, (long long)(th - t * p.H) + p.origin[1]);
+      whole(2, (long long)(n - th * p.W) + p.origin[2]);
+      whole(3, 0);
+    } else {
+      const long long o = (long long)b * p.pos_batch + (long long)n * p.axes;
+#pragma unroll
+      for (int a = 0; a < kRopeAxes; ++a) {
+        const bool there = a < p.axes;
+        if (p.pos_kind == 1) {
+          whole(a, there ? static_cast<const int*>(p.pos)[o + a] : 0);
+        } else {
+          const float v = there ? static_cast<const float*>(p.pos)[o + a] : 0.f, f = floorf(v);
+          whole(a, (long long)f);
+          rest[a] = (uint32_t)((v - f) * 4294967296.f);
+          bad[a] = v - v;
+        }
+      }
+    }
+  }
+  template <typename V>
+  __device__ __forceinline__ static V pick(const V (&v)[kRopeAxes], int a) {
+    return a == 0 ? v[0] : a == 1 ? v[1] : a == 2 ? v[2] : v[3];
+  }
+};
+
+// Sine and cosine of a pair's angle. The nearest quarter of a turn is taken off
+// and what is left, at most an eighth of a turn, goes into the Taylor
+// polynomials (to x^9 and x^8: 2e-9 and 3e-8 at the ends).
+__device__ __forceinline__ void pair_turn(const RopeParams& p, const RopePair& f, const Positions& pos, float* sn,
+                                          float* cs) {
+  const uint32_t lo = Positions::pick(pos.low, f.axis);
+  uint32_t t = __umulhi(lo, f.lo) + lo * f.hi + (uint32_t)Positions::pick(pos.high, f.axis) * f.lo;
+  if (p.pos_kind == 2) {
+    const uint32_t rest = Positions::pick(pos.rest, f.axis);
+    t += __umulhi(rest, f.hi) + rest * f.whole;
+  }
+  const int quarter = (int)((t + (1u << 29)) >> 30);
+  float x = (float)(int)(t - ((uint32_t)quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  if (p.pos_kind == 2) x += Positions::pick(pos.bad, f.axis);
+  const float x2 = x * x;
+  const float sine = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+  const float cosine = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+  const float u = quarter & 1 ? cosine : sine, v = quarter & 1 ? sine : cosine;
+  *sn = quarter & 2 ? -u : u;
+  *cs = (quarter + 1) & 2 ? -v : v;
+}
+
 // One thread's place in a tile and its rotation coefficients.
 template <typename T, int L, bool INTER>
 struct Place {
@@ -163,10 +227,8 @@ struct Place {
     }
   }
 
-  // Coefficients for the token's positions (as fp64, one per axis). `back`
-  // turns the other way.
-  __device__ __forceinline__ void angles(const double* freq, const int* axis, const double (&pos)[kRopeAxes], int rot,
-                                         bool back) {
+  // Coefficients for the token's positions. `back` turns the other way.
+  __device__ __forceinline__ void angles(const RopeParams& p, const RopePair* pairs, const Positions& pos, bool back) {
     const float dir = back ? -1.f : 1.f;
     if (INTER) {
 #pragma unroll
@@ -175,7 +237,7 @@ struct Place {
         s[2 * i] = s[2 * i + 1] = 0.f;
         if (turned >> (2 * i) & 1u) {
           float sn, cs;
-          turn(freq, axis, pos, chunk * 4 + i, &sn, &cs);
+          pair_turn(p, pairs[chunk * 4 + i], pos, &sn, &cs);
           c[2 * i] = c[2 * i + 1] = cs;
           s[2 * i] = -dir * sn;
           s[2 * i + 1] = dir * sn;
@@ -183,13 +245,13 @@ struct Place {
       }
     } else {
       // the two chunks of a pair of halves need the same eight angles: each computes four
-      const int first = (chunk * 8) % (rot > 0 ? rot / 2 : 1) + (sign < 0.f ? 0 : 4);
+      const int first = (chunk * 8) % (p.rot > 0 ? p.rot / 2 : 1) + (sign < 0.f ? 0 : 4);
       float cs[4], sn[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         cs[i] = 1.f;
         sn[i] = 0.f;
-        if (turned) turn(freq, axis, pos, first + i, &sn[i], &cs[i]);
+        if (turned) pair_turn(p, pairs[first + i], pos, &sn[i], &cs[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -200,25 +262,6 @@ struct Place {
         s[i + 4] = sign * dir * (sign < 0.f ? os : sn[i]);
       }
     }
-  }
-
-  // Sine and cosine of p freq quarter turns. The nearest whole number of them is
-  // taken off in fp64 (adding 1.5 x 2^52 leaves it in the low bits), and what
-  // is left, at most an eighth of a turn, goes into the Taylor polynomials
-  // (to x^9 and x^8: 2e-9 and 3e-8 at the ends).
-  __device__ __forceinline__ static void turn(const double* freq, const int* axis, const double (&pos)[kRopeAxes],
-                                              int j, float* sn, float* cs) {
-    constexpr double kWhole = 6755399441055744.0;
-    const int a = axis[j];
-    const double p = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-    const double q = p * freq[j], near = q + kWhole;
-    const float x = (float)(q - (near - kWhole)) * 1.57079632679489662f, x2 = x * x;
-    const int quarter = __double2loint(near);
-    const float sine = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
-    const float cosine = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
-    const float u = quarter & 1 ? cosine : sine, v = quarter & 1 ? sine : cosine;
-    *sn = quarter & 2 ? -u : u;
-    *cs = (quarter + 1) & 2 ? -v : v;
   }
 
   // The other channel of each pair (0 where a channel is not rotated, so that
@@ -245,32 +288,9 @@ struct Place {
   }
 };
 
-// The token's positions: the raster grid's (t, h, w), or the caller's list.
-__device__ __forceinline__ void token_positions(const RopeParams& p, int b, int n, double (&pos)[kRopeAxes]) {
-#pragma unroll
-  for (int a = 0; a < kRopeAxes; ++a) pos[a] = 0.0;
-  if (p.pos_kind == 0) {
-    const unsigned un = n, uw = p.W, uh = p.H;
-    const unsigned th = un / uw, t = th / uh;
-    pos[0] = (double)((long long)t + p.origin[0]);
-    pos[1] = (double)((long long)(th - t * uh) + p.origin[1]);
-    pos[2] = (double)((long long)(un - th * uw) + p.origin[2]);
-  } else {
-    const long long o = (long long)b * p.pos_batch + (long long)n * p.axes;
-#pragma unroll
-    for (int a = 0; a < kRopeAxes; ++a)
-      if (a < p.axes)
-        pos[a] = p.pos_kind == 1 ? (double)static_cast<const int*>(p.pos)[o + a]
-                                 : (double)static_cast<const float*>(p.pos)[o + a];
-  }
-}
-
-// Frequencies (in quarter turns) and axes from the launch parameters to shared memory.
-__device__ __forceinline__ void stage_rotation(const RopeParams& p, double* freq, int* axis) {
-  for (int j = threadIdx.x; j < p.rot / 2; j += kThreads) {
-    freq[j] = p.freq[j];
-    axis[j] = p.axis[j];
-  }
+// The pairs from the launch parameters to shared memory.
+__device__ __forceinline__ void stage_rotation(const RopeParams& p, RopePair* pairs) {
+  for (int j = threadIdx.x; j < p.rot / 2; j += kThreads) pairs[j] = p.pairs[j];
   __syncthreads();
 }
 
@@ -278,11 +298,11 @@ __device__ __forceinline__ void stage_rotation(const RopeParams& p, double* freq
 struct Unit {
   int b, tile, lo, hi;
   __device__ __forceinline__ Unit(const RopeParams& p, unsigned u) {
-    const unsigned g = u % p.groups, bt = u / p.groups, heads = p.t[0].heads + p.t[1].heads;
-    b = (int)(bt / p.tiles);
+    const unsigned bt = p.by_groups(u), g = u - bt * p.groups, heads = p.t[0].heads + p.t[1].heads;
+    b = (int)p.by_tiles(bt);
     tile = (int)(bt - (unsigned)b * p.tiles);
-    lo = (int)(heads * g / p.groups);
-    hi = (int)(heads * (g + 1) / p.groups);
+    lo = (int)p.by_groups(heads * g);
+    hi = (int)p.by_groups(heads * (g + 1));
   }
   // Its heads of tensor t.
   __device__ __forceinline__ int first(const RopeParams& p, int t) const { return max(lo - (t ? p.t[0].heads : 0), 0); }
@@ -389,24 +409,22 @@ struct Feed {
 template <typename T, int L, bool INTER, int U>
 __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int STAGES = 3;
-  __shared__ double freq[kRopePairs];
-  __shared__ int axis[kRopePairs];
+  __shared__ RopePair pairs[kRopePairs];
   __shared__ uint4 ring[STAGES][Feed<T, U, false, STAGES>::SLOTS][kThreads];
   constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
   Feed<T, U, false, STAGES> feed;
   feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
-  stage_rotation(p, freq, axis);
+  stage_rotation(p, pairs);
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
   for (unsigned u = blockIdx.x; u < p.units; u += gridDim.x) {
     const Unit w(p, u);
     const int n = w.tile * ROWS + me.lane_row;
     const bool live = n < p.N && me.in_row;
-    double pos[kRopeAxes];
-    token_positions(p, w.b, n < p.N ? n : 0, pos);
-    me.angles(freq, axis, pos, p.rot, p.back != 0);
+    const Positions pos(p, w.b, n < p.N ? n : 0);
+    me.angles(p, pairs, pos, p.back != 0);
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       const RopeTensor& x = p.t[t];
@@ -477,8 +495,7 @@ template <typename T, int L, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
   constexpr int STAGES = kBackwardStages;
   extern __shared__ uint4 ring[];
-  __shared__ double freq[kRopePairs];
-  __shared__ int axis[kRopePairs];
+  __shared__ RopePair pairs[kRopePairs];
   __shared__ float part[2][8][kThreads];  // a thread's sums of 8 channels over its rows so far
   constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
@@ -486,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
   Feed<T, 2, true, STAGES> feed;
   ptx::let_next_start();
   feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
-  stage_rotation(p, freq, axis);
+  stage_rotation(p, pairs);
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
 #pragma unroll
@@ -495,9 +512,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
     const Unit w(p, u);
     const int n = w.tile * ROWS + me.lane_row;
     const bool live = n < p.N && me.in_row;
-    double pos[kRopeAxes];
-    token_positions(p, w.b, n < p.N ? n : 0, pos);
-    me.angles(freq, axis, pos, p.rot, true);
+    const Positions pos(p, w.b, n < p.N ? n : 0);
+    me.angles(p, pairs, pos, true);
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       const RopeTensor& x = p.t[t];
@@ -603,12 +619,14 @@ int plan_units(RopeParams& p, int num_sms, int per_sm, int angles) {
   const long long tiles = (long long)p.tiles * p.B, slots = (long long)num_sms * per_sm;
   long long best = -1;
   p.groups = 1;
-  for (int g = 1; g <= heads && tiles * g < (1LL << 31); ++g) {
+  for (int g = 1; g <= heads && tiles * g < (1LL << 31) && heads * (g + 1LL) < (1LL << 31); ++g) {
     const long long rounds = (tiles * g + slots - 1) / slots;
     const long long cost = rounds * (angles + (heads + g - 1) / g);
     if (best < 0 || cost < best) best = cost, p.groups = g;
   }
   p.units = (unsigned)(tiles * p.groups);
+  p.by_groups = Divisor(p.groups);
+  p.by_tiles = Divisor(p.tiles);
   return (int)(p.units < slots ? p.units : slots);
 }
 

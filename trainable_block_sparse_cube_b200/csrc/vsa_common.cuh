@@ -166,15 +166,35 @@ struct RopeTensor {
   long long in_b, in_h, in_n, dy_b, dy_h, dy_n, out_b, out_h, out_n;
 };
 
+// Division of numbers below 2^31 by a number known on the host:
+// n / d = n m >> s, m the whole number above 2^s / d, s = 31 + log2 d rounded up.
+struct Divisor {
+  uint32_t m = 0;
+  int s = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t d) {
+    for (s = 31; (1ull << (s - 31)) < d; ++s) {}
+    m = (uint32_t)((1ull << s) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (uint32_t)((uint64_t)n * m >> s); }
+};
+
+// One pair of channels: the axis it turns with, and how far for one position.
+struct RopePair {
+  uint32_t lo, hi;  // fraction of a turn, in 2^-64
+  uint32_t whole;   // whole turns, modulo 2^32 (they count between whole positions)
+  int axis;
+};
+
 struct RopeParams {
   RopeTensor t[2];          // q, k
   int B, N, D;
   int rot, interleaved;     // rotated leading channels; pairs (2i, 2i + 1) or (i, i + rot/2)
   int axes;
-  double freq[kRopePairs];  // quarter turns (radians x 2 / pi) per unit of position
-  int axis[kRopePairs];
+  RopePair pairs[kRopePairs];
   int pos_kind;             // 0: raster grid of H x W frames; 1: int32 list; 2: fp32 list
   int H, W, origin[3];
+  Divisor by_h, by_w;       // of a raster grid
   const void* pos;          // list [B or 1, N, axes]
   long long pos_batch;      // elements between batches of the list (0: one list for all)
   int back;                 // rotate by the opposite angle
@@ -183,6 +203,7 @@ struct RopeParams {
   float* partial;           // norm backward: [grid, 2, D] weight gradients of the blocks
   int tiles, groups;        // work split, set by the launcher
   unsigned units;
+  Divisor by_groups, by_tiles;
 };
 
 cudaError_t launch_rope(RopeParams p, int type, int num_sms, cudaStream_t st);
