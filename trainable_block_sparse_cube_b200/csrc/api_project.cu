@@ -21,6 +21,7 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
   if (r->rot < 0 || r->rot > s->D || r->rot % 2) return VSA_ERR_SHAPE;
   if (!r->interleaved && r->rot % 16) return VSA_ERR_UNSUPPORTED;
   if (r->axes < 1 || r->axes > VSA_ROPE_MAX_AXES) return VSA_ERR_UNSUPPORTED;
+  p->wide = 1;
   p->B = s->B;
   p->N = s->N;
   p->D = s->D;
@@ -75,6 +76,7 @@ vsa_status add_tensor(vsa::RopeParams* p, int t, int elem, const vsa_heads* in, 
   x.heads = in->heads;
   x.in_b = in->s_b, x.in_h = in->s_h, x.in_n = in->s_n;
   x.out_b = out->s_b, x.out_h = out->s_h, x.out_n = out->s_n;
+  if ((reinterpret_cast<uintptr_t>(out->data) & 31u) || (out->s_b % 8 | out->s_h % 8 | out->s_n % 8)) p->wide = 0;
   if (dy) x.dy = dy->data, x.dy_b = dy->s_b, x.dy_h = dy->s_h, x.dy_n = dy->s_n;
   return VSA_OK;
 }

@@ -108,10 +108,21 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
 }
+// fp32: whole 32-byte sectors where `wide` says that they are aligned.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8], bool) {
+  store8(p, x);
+}
 template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8<float>(float* p, const float (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
 }
 
 template <typename T>
@@ -313,34 +324,44 @@ struct Unit {
 
 // The rows that a thread will need, in the order in which it will need them: U
 // heads a step (zeros where there are fewer, or no such token), through all
-// its units. Each step's pieces go to the thread's own slots of a stage, so no
-// barrier is needed; a stage is filled again one step after it was read. The
+// its units. Each step's 16-byte pieces go to the thread's own slots of a
+// stage, so no barrier is needed; a stage is filled again one step after it
+// was read. A thread's 8 fp32 channels are two pieces, and there the lanes of
+// a row copy for one another, each two pieces L apart: neighbours' pieces are
+// then neighbours in memory and in the row's slots, and no 32-byte sector is
+// read twice. The
 // common step is a handful of instructions: addresses are kept up by
 // additions (products and checks for every row were half of all instructions).
-template <typename T, int U, bool DY, int STAGES>
+template <typename T, int L, int U, bool DY, int STAGES>
 struct Feed {
   static constexpr int PIECES = (int)sizeof(T) / 2;  // 16-byte pieces of 8 channels
   static constexpr int SLOTS = U * (DY ? 2 : 1) * PIECES;
   static constexpr uint32_t STAGE = SLOTS * kThreads * 16, END = STAGES * STAGE;
   uint32_t mine, in, out;  // shared address of the thread's first slot; offsets of the stages filled and read next
+  uint32_t target[PIECES]; // where its copies go, for the first row of a stage
+  int ahead;               // elements between its copies
   unsigned u;
   int t, left;             // heads left in the tensor's part of the unit
   const T *src, *dsrc;
   long long step, dstep;   // elements between heads
-  uint32_t bytes;          // 16, or 0 for a thread outside the tensor
+  uint32_t bytes[PIECES];  // 16, or 0 for a piece outside the tensor
 
-  __device__ __forceinline__ void start(const RopeParams& p, const void* smem, int rows, int lane_row, int chunk,
-                                        bool in_row) {
-    mine = ptx::smem_u32(smem) + threadIdx.x * 16;
+  __device__ __forceinline__ void start(const RopeParams& p, const void* smem, int rows, int lane_row, int chunk) {
+    mine = ptx::smem_u32(smem) + threadIdx.x * 16 * PIECES;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      target[i] = mine + (chunk + L * i - chunk * PIECES) * 16;
+    }
+    ahead = L * 4;
     in = out = 0;
     u = blockIdx.x;
     t = -1;
     left = 0;
-    for (int i = 0; i < STAGES - 1; ++i) load(p, rows, lane_row, chunk, in_row);
+    for (int i = 0; i < STAGES - 1; ++i) load(p, rows, lane_row, chunk);
   }
 
   // The next tensor or unit that has heads.
-  __device__ __forceinline__ void open(const RopeParams& p, int rows, int lane_row, int chunk, bool in_row) {
+  __device__ __forceinline__ void open(const RopeParams& p, int rows, int lane_row, int chunk) {
     do {
       if (++t == 2) t = 0, u += gridDim.x;
       if (u >= p.units) return;
@@ -348,10 +369,11 @@ struct Feed {
       const RopeTensor& x = p.t[t];
       const int lo = w.first(p, t), n = w.tile * rows + lane_row;
       left = w.last(p, t) - lo;
-      const bool live = n < p.N && in_row;
-      bytes = live ? 16 : 0;
-      // a thread outside reads nothing, and keeps an address inside
-      const long long at = lo, b = live ? w.b : 0, m = live ? n : 0, c = live ? chunk * 8 : 0;
+      const bool live = n < p.N && chunk * (16 / (int)sizeof(T)) < p.D;
+      // what lies outside is not read, and keeps an address inside
+      const long long at = lo, b = live ? w.b : 0, m = live ? n : 0, c = live ? chunk * (16 / (int)sizeof(T)) : 0;
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) bytes[i] = live && (chunk + L * i) * (16 / (int)sizeof(T)) < p.D ? 16 : 0;
       src = static_cast<const T*>(x.in) + b * x.in_b + m * x.in_n + at * x.in_h + c;
       step = x.in_h;
       if (DY) {
@@ -366,18 +388,18 @@ struct Feed {
   }
 
   // Copies of the next step, one group (an empty one behind the last).
-  __device__ __forceinline__ void load(const RopeParams& p, int rows, int lane_row, int chunk, bool in_row) {
-    if (left <= 0 && u < p.units) open(p, rows, lane_row, chunk, in_row);
+  __device__ __forceinline__ void load(const RopeParams& p, int rows, int lane_row, int chunk) {
+    if (left <= 0 && u < p.units) open(p, rows, lane_row, chunk);
     if (u < p.units) {
-      const uint32_t dst = mine + in;
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         const bool there = k < left;
-        const uint32_t n = there ? bytes : 0;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-          copy(dst + (k * PIECES + i) * kThreads * 16, src + i * 4, n);
-          if (DY) copy(dst + ((U + k) * PIECES + i) * kThreads * 16, dsrc + i * 4, n);
+          const uint32_t dst = target[i] + in + k * PIECES * kThreads * 16, n = there ? bytes[i] : 0;
+          const int far = n ? i * ahead : 0;
+          copy(dst, src + far, n);
+          if (DY) copy(dst + U * PIECES * kThreads * 16, dsrc + far, n);
         }
         if (there) {
           src += step;
@@ -391,14 +413,17 @@ struct Feed {
   }
 
   // The oldest step's rows have arrived.
-  __device__ __forceinline__ void wait() { ptx::cp_async_wait<STAGES - 2>(); }
+  __device__ __forceinline__ void wait() {
+    ptx::cp_async_wait<STAGES - 2>();
+    if (PIECES > 1) __syncwarp();
+  }
   __device__ __forceinline__ Row8<T> row(int k) const {
     Row8<T> v;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(v.r[4 * i]), "=r"(v.r[4 * i + 1]), "=r"(v.r[4 * i + 2]), "=r"(v.r[4 * i + 3])
-                   : "r"(mine + out + (k * PIECES + i) * kThreads * 16)
+                   : "r"(mine + out + k * PIECES * kThreads * 16 + i * 16)
                    : "memory");
     return v;
   }
@@ -410,12 +435,12 @@ template <typename T, int L, bool INTER, int U>
 __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int STAGES = 3;
   __shared__ RopePair pairs[kRopePairs];
-  __shared__ uint4 ring[STAGES][Feed<T, U, false, STAGES>::SLOTS][kThreads];
+  __shared__ uint4 ring[STAGES][Feed<T, L, U, false, STAGES>::SLOTS][kThreads];
   constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
-  Feed<T, U, false, STAGES> feed;
-  feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
+  Feed<T, L, U, false, STAGES> feed;
+  feed.start(p, ring, ROWS, me.lane_row, me.chunk);
   stage_rotation(p, pairs);
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
 #pragma unroll
         for (int k = 0; k < U; ++k) now[k] = feed.row(k);
         feed.next();
-        feed.load(p, ROWS, me.lane_row, me.chunk, me.in_row);
+        feed.load(p, ROWS, me.lane_row, me.chunk);
         F2 o[U / 2][8], r[U / 2];
 #pragma unroll
         for (int k = 0; k < U / 2; ++k) {
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
           float a[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) a[i] = k & 1 ? split2(o[k / 2][i]).y : split2(o[k / 2][i]).x;
-          if (live && h0 + k < heads) store8(dst, a);
+          if (live && h0 + k < heads) store8(dst, a, p.wide != 0);
           dst += step;
         }
       }
@@ -500,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
   constexpr int ROWS = kThreads / L;
   Place<T, L, INTER> me;
   me.init(p.D, p.rot);
-  Feed<T, 2, true, STAGES> feed;
+  Feed<T, L, 2, true, STAGES> feed;
   ptx::let_next_start();
-  feed.start(p, ring, ROWS, me.lane_row, me.chunk, me.in_row);
+  feed.start(p, ring, ROWS, me.lane_row, me.chunk);
   stage_rotation(p, pairs);
   const float inv_d = 1.f / (float)p.D;
   const bool full = p.rot == p.D;
@@ -537,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
           const Row8<T> d0 = feed.row(2), d1 = feed.row(3);
           unpack_pair(feed.row(0), feed.row(1), v);
           feed.next();
-          feed.load(p, ROWS, me.lane_row, me.chunk, me.in_row);
+          feed.load(p, ROWS, me.lane_row, me.chunk);
           unpack_pair(d0, d1, d);
           me.other(d0, d1, d, full, o);
 #pragma unroll
@@ -567,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_k
           const float2 f = split2(v[i]);
           a[i] = f.x, b[i] = f.y;
         }
-        if (live) store8(dst, a);
+        if (live) store8(dst, a, p.wide != 0);
         dst += step;
-        if (second) store8(dst, b);
+        if (second) store8(dst, b, p.wide != 0);
         dst += step;
       }
 #pragma unroll
@@ -634,7 +659,7 @@ template <typename T, int L, bool INTER>
 cudaError_t launch_typed(const RopeParams& p, bool backward, int grid, cudaStream_t st) {
   constexpr int U = sizeof(T) == 4 ? 2 : 4;
   if (backward) {
-    constexpr int smem = Feed<T, 2, true, kBackwardStages>::END;
+    constexpr int smem = Feed<T, L, 2, true, kBackwardStages>::END;
     const cudaError_t e = allow_smem<norm_rope_backward_kernel<T, L, INTER>>(smem);
     if (e != cudaSuccess) return e;
     norm_rope_backward_kernel<T, L, INTER><<<grid, kThreads, smem, st>>>(p);

@@ -200,6 +200,7 @@ struct RopeParams {
   int back;                 // rotate by the opposite angle
   int norm;
   float eps;
+  int wide;                 // every 8 fp32 channels of the outputs start on a 32-byte boundary
   float* partial;           // norm backward: [grid, 2, D] weight gradients of the blocks
   int tiles, groups;        // work split, set by the launcher
   unsigned units;
