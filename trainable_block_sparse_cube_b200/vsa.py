@@ -641,7 +641,7 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, rotation, gr
     dwq = None if q_weight is None else torch.empty_like(q_weight)
     dwk = None if k is None or k_weight is None else torch.empty_like(k_weight)
     nb = L.vsa_qk_norm_rope_backward_workspace_bytes(D)
-    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    ws = q.new_empty(nb // q.element_size())
     _check(L.vsa_qk_norm_rope_backward(sizes, rotation._packed, where, hq, hk, _address(q_weight), _address(k_weight),
                                        eps, gq, gk, oq, ok, _address(dwq), _address(dwk), ws.data_ptr(), nb,
                                        _stream()), "vsa_qk_norm_rope_backward")
@@ -717,7 +717,7 @@ def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out
         ho = _pack_heads(out.data_ptr(), 1, N * F, 0, F) if heads is None else \
             _pack_heads(out.data_ptr(), heads, N * F, N * shape[3], shape[3])
     nb = L.vsa_linear_workspace_bytes(sizes)
-    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    ws = x.new_empty(nb // 2) if nb else None
     _check(L.vsa_linear(sizes, hx, weight.data_ptr(), weight.stride(0), _address(bias), ACTIVATIONS[activation], hr, hz,
                         ho, _address(ws), nb, _stream()), "vsa_linear")
     return out
@@ -746,9 +746,9 @@ def linear_backward(x, weight, dout, z=None, activation=None, bias=False, dx=Non
         dx = torch.empty_like(x)
         hd = _need_rows(dx, "dx")
     dw = torch.empty_like(weight, memory_format=torch.contiguous_format) if want[1] else None
-    db = torch.empty(F, dtype=torch.float32, device=device) if bias else None
+    db = x.new_empty(F, dtype=torch.float32) if bias else None
     nb = L.vsa_linear_backward_workspace_bytes(sizes, ACTIVATIONS[activation])
-    ws = torch.empty(nb, dtype=torch.uint8, device=device) if nb else None
+    ws = x.new_empty(nb // 2) if nb else None
     _check(L.vsa_linear_backward(sizes, hx, weight.data_ptr(), weight.stride(0), hz, ACTIVATIONS[activation], hg, hd,
                                  _address(dw), _address(db), _address(ws), nb, _stream()), "vsa_linear_backward")
     return dx, dw, db
