@@ -233,6 +233,11 @@ __device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8], bool wid
   }
 }
 
+// Brings a line into L1.
+__device__ __forceinline__ void touch(const float* p) {
+  asm volatile("{\n\t.reg .b32 t;\n\tld.global.ca.b32 t, [%0];\n\t}" ::"l"(p) : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ T* view_at(const RowsView& v, int b, int head, int n) {
   return static_cast<T*>(v.data) + b * v.s_b + head * v.s_h + n * v.s_n;
@@ -468,72 +473,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
     }
   } else {
     // ---- epilogue: a warp takes 32 rows, a row a lane, and one half of the tile's
-    // columns, 32 at a time, from tensor memory straight to global memory
-    // in whole 32-byte sectors. Shared memory has no bandwidth to spare: the
-    // MMAs read 64 bytes a cycle of it and the loads write as many (%STG%).
+    // columns, 32 at a time, from tensor memory straight to global memory in
+    // whole 32-byte sectors. Shared memory has no bandwidth to spare: the MMAs
+    // read 64 bytes a cycle of it and the loads write as many (%STG%).
     const int quarter = warp & 3, groups = p.bn / 32;
     const int g0 = warp < 7 ? 0 : (groups + 1) / 2, g1 = warp < 7 ? (groups + 1) / 2 : groups;
+    const bool plain = !p.bias && !p.z.data && !p.residual.data && p.act == kActNone, wide = p.wide != 0;
     int tile = 0;
     for (unsigned u = pair; u < units; u += pairs, ++tile) {
       const Unit w(p, u);
       const int buf = tile & 1;
+      const int in_tile = (int)rank * 128 + quarter * 32 + lane, n = w.row0 + in_tile;
+      const bool live = n < p.rows, some = n - lane < p.rows;
+      const uint32_t acc0 = tmem_addr(tmem, quarter * 32, buf * kAccColumns);
+      const int first = w.col0 + g0 * 32;
+      // its part of the bias is in L1 by the time the tile is there
+      if (p.bias && lane < 4 && some && first + lane * 32 < p.F) touch(p.bias + first + lane * 32);
+      T* const out = view_at<T>(p.out, w.batch, 0, n);
       if (!wait.warp(&sh.acc_full[buf], (tile >> 1) & 1)) break;
       tc_fence_after();
-      const int in_tile = (int)rank * 128 + quarter * 32 + lane, n = w.row0 + in_tile;
-      const bool live = n < p.rows;
+      if (w.part >= 0) {  // a part of the contraction: fp32 sums
+        float* const dst = p.partial + ((long long)w.part * 256 + in_tile) * p.bn;
 #pragma unroll 1
-      for (int g = g0; g < g1; ++g) {
-        const int col = w.col0 + g * 32, left = p.F - col;  // columns up to the edge, a multiple of 8
-        if (n - lane >= p.rows || left <= 0) break;
-        uint32_t r[32];
-        const uint32_t acc = tmem_addr(tmem, quarter * 32, buf * kAccColumns + g * 32);
-        if (w.part >= 0) {  // a part of the contraction: fp32 sums
-          tmem_ld32(acc, r);
+        for (int g = g0; g < g1 && some && w.col0 + g * 32 < p.F; ++g) {
+          uint32_t r[32];
+          tmem_ld32(acc0 + g * 32, r);
           tmem_wait_ld();
-          float* const dst = p.partial + ((long long)w.part * 256 + in_tile) * p.bn + g * 32;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = r[8 * j + i];
-            if (live) store32(dst + 8 * j, v, p.wide, true);
+            const uint32_t v[8] = {r[8 * j],     r[8 * j + 1], r[8 * j + 2], r[8 * j + 3],
+                                   r[8 * j + 4], r[8 * j + 5], r[8 * j + 6], r[8 * j + 7]};
+            if (live) store32(dst + g * 32 + 8 * j, v, wide, true);
           }
-          continue;
         }
-        const int head = p.out.heads > 1 ? col / p.out.D : 0, ch = col - head * p.out.D;
-        uint32_t x[2][8];
-        if (p.residual.data) {
-          const T* const src = view_at<T>(p.residual, w.batch, head, n) + ch;
+      } else if (plain) {
+#pragma unroll 1
+        for (int g = g0; g < g1; g += 2) {
+          const int col = w.col0 + g * 32, left = p.F - col;  // columns up to the edge, a multiple of 8
+          if (!some || left <= 0) break;
+          const bool two = g + 1 < g1;
+          uint32_t r[64];
+          tmem_ld32(acc0 + g * 32, reinterpret_cast<uint32_t (&)[32]>(r[0]));
+          if (two) tmem_ld32(acc0 + g * 32 + 32, reinterpret_cast<uint32_t (&)[32]>(r[32]));
+          tmem_wait_ld();
+          const int head = p.out.heads > 1 ? col / p.out.D : 0;
+          T* const dst = out + head * p.out.s_h + (col - head * p.out.D);
+          // a second group lies in the next head only where heads are 64 wide and the first is their second half
+          const bool turn = two && p.out.heads > 1 && (col + 32) % p.out.D == 0;
+          T* const dst2 = turn ? out + (head + 1) * p.out.s_h : dst + 32;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (live && 16 * j < left) load32(src + 16 * j, x[j], p.wide, left > 16 * j + 8);
-        }
-        tmem_ld32(acc, r);
-        tmem_wait_ld();
+          for (int j = 0; j < 4; ++j) {
+            if ((j < 2 || two) && 16 * j < left) {
+              float v[16];
+              uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (16 * j >= left) break;
-          const bool both = left > 16 * j + 8;
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
-          if (p.bias) add_bias16(v, p.bias + col + 16 * j, both);
-          uint32_t o[8];
-          if (p.z.data) {
-            pack16<T>(v, o);
-            if (live) store32(view_at<T>(p.z, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
-          }
-          activate_n(v, p.act);
-          if (p.residual.data) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = unpack2<T>(x[j][i]);
-              v[2 * i] += f.x;
-              v[2 * i + 1] += f.y;
+              for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
+              pack16<T>(v, o);
+              if (live) store32(j < 2 ? dst + 16 * j : dst2 + 16 * (j - 2), o, wide, left > 16 * j + 8);
             }
           }
-          pack16<T>(v, o);
-          if (live) store32(view_at<T>(p.out, w.batch, head, n) + ch + 16 * j, o, p.wide, both);
+        }
+      } else {
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g) {
+          const int col = w.col0 + g * 32, left = p.F - col;
+          if (!some || left <= 0) break;
+          uint32_t r[32];
+          tmem_ld32(acc0 + g * 32, r);
+          const int head = p.out.heads > 1 ? col / p.out.D : 0, ch = col - head * p.out.D;
+          uint32_t x[2][8];
+          if (p.residual.data) {
+            const T* const src = view_at<T>(p.residual, w.batch, head, n) + ch;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (live && 16 * j < left) load32(src + 16 * j, x[j], wide, left > 16 * j + 8);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (16 * j >= left) break;
+            const bool both = left > 16 * j + 8;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
+            if (p.bias) add_bias16(v, p.bias + col + 16 * j, both);
+            uint32_t o[8];
+            if (p.z.data) {
+              pack16<T>(v, o);
+              if (live) store32(view_at<T>(p.z, w.batch, head, n) + ch + 16 * j, o, wide, both);
+            }
+            activate_n(v, p.act);
+            if (p.residual.data) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 f = unpack2<T>(x[j][i]);
+                v[2 * i] += f.x;
+                v[2 * i + 1] += f.y;
+              }
+            }
+            pack16<T>(v, o);
+            if (live) store32(out + head * p.out.s_h + ch + 16 * j, o, wide, both);
+          }
         }
       }
       tc_fence_before();
