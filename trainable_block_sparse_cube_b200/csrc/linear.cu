@@ -193,14 +193,6 @@ __device__ __forceinline__ void add_bias8(float (&v)[8], const float* bias) {
   v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
 }
 
-__device__ __forceinline__ void add_bias16(float (&v)[16], const float* bias, bool both) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= 2 && !both) break;
-    const float4 a = __ldg(reinterpret_cast<const float4*>(bias) + i);
-    v[4 * i] += a.x, v[4 * i + 1] += a.y, v[4 * i + 2] += a.z, v[4 * i + 3] += a.w;
-  }
-}
 template <typename T>
 __device__ __forceinline__ void pack16(const float (&v)[16], uint32_t (&o)[8]) {
 #pragma unroll
@@ -233,9 +225,11 @@ __device__ __forceinline__ void load32(const void* p, uint32_t (&v)[8], bool wid
   }
 }
 
-// Brings a line into L1.
-__device__ __forceinline__ void touch(const float* p) {
-  asm volatile("{\n\t.reg .b32 t;\n\tld.global.ca.b32 t, [%0];\n\t}" ::"l"(p) : "memory");
+// Asked for here and not where it is used.
+__device__ __forceinline__ float4 load_bias(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
 }
 
 template <typename T>
@@ -486,10 +480,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
       const int in_tile = (int)rank * 128 + quarter * 32 + lane, n = w.row0 + in_tile;
       const bool live = n < p.rows, some = n - lane < p.rows;
       const uint32_t acc0 = tmem_addr(tmem, quarter * 32, buf * kAccColumns);
-      const int first = w.col0 + g0 * 32;
-      // its part of the bias is in L1 by the time the tile is there
-      if (p.bias && lane < 4 && some && first + lane * 32 < p.F) touch(p.bias + first + lane * 32);
       T* const out = view_at<T>(p.out, w.batch, 0, n);
+      // The bias and the residual of a group are asked for one group ahead, of
+      // the first one before the tile is there.
+      const bool more = p.bias || p.residual.data;
+      float4 bias[8];
+      uint32_t res[2][8];
+      auto ask = [&](int g) {
+        const int col = w.col0 + g * 32, left = p.F - col;
+        if (!some || g >= g1 || left <= 0) return;
+        if (p.bias) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (4 * i < left) bias[i] = load_bias(p.bias + col + 4 * i);
+        }
+        if (p.residual.data && live) {
+          const int head = p.out.heads > 1 ? col / p.out.D : 0;
+          const T* const src = view_at<T>(p.residual, w.batch, head, n) + (col - head * p.out.D);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (16 * j < left) load32(src + 16 * j, res[j], wide, left > 16 * j + 8);
+        }
+      };
+      if (more && w.part < 0) ask(g0);
       if (!wait.warp(&sh.acc_full[buf], (tile >> 1) & 1)) break;
       tc_fence_after();
       if (w.part >= 0) {  // a part of the contraction: fp32 sums
@@ -541,37 +554,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) gemm_ke
           uint32_t r[32];
           tmem_ld32(acc0 + g * 32, r);
           const int head = p.out.heads > 1 ? col / p.out.D : 0, ch = col - head * p.out.D;
-          uint32_t x[2][8];
-          if (p.residual.data) {
-            const T* const src = view_at<T>(p.residual, w.batch, head, n) + ch;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (live && 16 * j < left) load32(src + 16 * j, x[j], wide, left > 16 * j + 8);
-          }
           tmem_wait_ld();
+          float v[2][16];
+          uint32_t x[2][8];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i / 16][i % 16] = __uint_as_float(r[i]);
+          if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float* const q = &v[i / 4][i % 4 * 4];
+              q[0] += bias[i].x, q[1] += bias[i].y, q[2] += bias[i].z, q[3] += bias[i].w;
+            }
+          }
+          if (p.residual.data) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i / 8][i % 8] = res[i / 8][i % 8];
+          }
+          if (more) ask(g + 1);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (16 * j >= left) break;
             const bool both = left > 16 * j + 8;
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[16 * j + i]);
-            if (p.bias) add_bias16(v, p.bias + col + 16 * j, both);
             uint32_t o[8];
             if (p.z.data) {
-              pack16<T>(v, o);
+              pack16<T>(v[j], o);
               if (live) store32(view_at<T>(p.z, w.batch, head, n) + ch + 16 * j, o, wide, both);
             }
-            activate_n(v, p.act);
+            activate_n(v[j], p.act);
             if (p.residual.data) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float2 f = unpack2<T>(x[j][i]);
-                v[2 * i] += f.x;
-                v[2 * i + 1] += f.y;
+                v[j][2 * i] += f.x;
+                v[j][2 * i + 1] += f.y;
               }
             }
-            pack16<T>(v, o);
+            pack16<T>(v[j], o);
             if (live) store32(out + head * p.out.s_h + ch + 16 * j, o, wide, both);
           }
         }
