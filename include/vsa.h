@@ -365,8 +365,8 @@ typedef struct {
  * pair j of them turns by pos[axis[j]] * freq[j] radians,
  *   (u, v) -> (u cos - v sin, u sin + v cos).
  * Pair j is channels (2j, 2j + 1) if interleaved, else (j, j + rot/2), and
- * then rot is a multiple of 16. freq is rounded nowhere: angles are formed in
- * double precision, so far positions lose nothing. */
+ * then rot is a multiple of 16. Angles are exact to 2^-32 of a turn at any
+ * position, so far positions lose nothing. */
 typedef struct {
   int rot, interleaved;
   int axes; /* 1 .. VSA_ROPE_MAX_AXES */

@@ -378,8 +378,8 @@ def test_the_block_around_the_attention(D):
     N, C = T * H * W, h * D
     rot = vsa.Rotation(D, (D // 2, D // 4, D // 4))
     hid = _randn(1, B, N, C, dtype=torch.bfloat16)
-    wqkv, wo = _randn(2, 3 * C, C, dtype=torch.bfloat16, std=C ** -0.5), _randn(3, C, C, dtype=torch.bfloat16, std=C ** -0.5)
-    wu, wd = _randn(4, 2 * C, C, dtype=torch.bfloat16, std=C ** -0.5), _randn(5, C, 2 * C, dtype=torch.bfloat16, std=C ** -0.5)
+    wqkv, wo, wu, wd = (_randn(2 + i, *s, dtype=torch.bfloat16, std=C ** -0.5)
+                        for i, s in enumerate(((3 * C, C), (C, C), (2 * C, C), (C, 2 * C))))
     bu = _randn(6, 2 * C, dtype=torch.float32)
     nq, nk = 1 + 0.2 * _randn(7, D, dtype=torch.float32), 1 + 0.2 * _randn(8, D, dtype=torch.float32)
     gc, gf = torch.full((B, h, N), 0.5, device="cuda"), torch.ones(B, h, N, device="cuda")
@@ -439,8 +439,7 @@ def test_the_block_around_the_attention(D):
     grads = torch.autograd.grad(out64, P, g.double())
     # Between the ends every tensor is rounded to bf16 once (relative half steps of 2^-8 that add up at random over
     # about ten tensors in a row): 10 half steps = 0.04 of the root mean square of a result bounds the error's.
-    for name, a, r in (("out", out, out64), ("dhid", dhid, grads[0]), ("dwqkv", dwqkv, grads[1]), ("dwo", dwo, grads[2]),
-                       ("dwu", dwu, grads[3]), ("dwd", dwd, grads[4]), ("dbu", dbu, grads[5]), ("dnq", dnq, grads[6]),
-                       ("dnk", dnk, grads[7])):
+    names = ("dhid", "dwqkv", "dwo", "dwu", "dwd", "dbu", "dnq", "dnk")
+    for name, a, r in [("out", out, out64), *zip(names, (dhid, dwqkv, dwo, dwu, dwd, dbu, dnq, dnk), grads)]:
         err = ((a.double() - r).square().mean() / r.square().mean()).sqrt().item()
         assert err <= 10 * 2.0 ** -8, (name, err)

@@ -52,20 +52,23 @@ def _sizes(**kw):
 
 
 def _view(channels, heads=1, **kw):
-    d = dict(data=1 << 20, heads=heads, s_b=64 * channels, s_h=64 * (channels // max(heads, 1)), s_n=channels // max(heads, 1))
+    D = channels // max(heads, 1)
+    d = dict(data=1 << 20, heads=heads, s_b=64 * channels, s_h=64 * D, s_n=D)
     d.update(kw)
     return vsa.Heads(*(d[n] for n, _ in vsa.Heads._fields_))
 
 
-def _forward(lib, sizes=None, x=None, w=1 << 20, stride=128, bias=None, act=0, res=None, z=None, out=None, ws=(1 << 20, 1 << 40)):
-    return lib.vsa_linear(_sizes() if sizes is None else sizes, _view(128) if x is None else x, w, stride, bias, act, res, z,
-                          _view(256) if out is None else out, *ws, None)
+def _forward(lib, sizes=None, x=None, w=1 << 20, stride=128, bias=None, act=0, res=None, z=None, out=None,
+             ws=(1 << 20, 1 << 40)):
+    return lib.vsa_linear(_sizes() if sizes is None else sizes, _view(128) if x is None else x, w, stride, bias, act,
+                          res, z, _view(256) if out is None else out, *ws, None)
 
 
 def _backward(lib, sizes=None, x=None, w=1 << 20, stride=128, z=None, act=0, dout=None, dx=None, dw=1 << 20, db=None,
               ws=(1 << 20, 1 << 40)):
-    return lib.vsa_linear_backward(_sizes() if sizes is None else sizes, _view(128) if x is None else x, w, stride, z, act,
-                                   _view(256) if dout is None else dout, _view(128) if dx is None else dx, dw, db, *ws, None)
+    return lib.vsa_linear_backward(_sizes() if sizes is None else sizes, _view(128) if x is None else x, w, stride, z,
+                                   act, _view(256) if dout is None else dout, _view(128) if dx is None else dx, dw, db,
+                                   *ws, None)
 
 
 @pytest.mark.parametrize("call", [_forward, _backward])
@@ -75,7 +78,8 @@ def _backward(lib, sizes=None, x=None, w=1 << 20, stride=128, z=None, act=0, dou
     (dict(sizes=_sizes(K=100)), 3), (dict(sizes=_sizes(F=12)), 3), (dict(sizes=_sizes(F=1 << 21)), 3),
     (dict(sizes=_sizes(B=1 << 12, N=1 << 19)), 3),
     (dict(act=4), 3), (dict(act=-1), 3),
-    (dict(w=None), 1), (dict(w=(1 << 20) + 8), 4), (dict(stride=120), 1), (dict(stride=132), 4), (dict(stride=1 << 39), 3),
+    (dict(w=None), 1), (dict(w=(1 << 20) + 8), 4), (dict(stride=120), 1), (dict(stride=132), 4),
+    (dict(stride=1 << 39), 3),
     (dict(x=_view(128, data=None)), 1), (dict(x=_view(128, data=(1 << 20) + 8)), 4), (dict(x=_view(128, heads=0)), 2),
     (dict(x=_view(128, heads=3)), 2), (dict(x=_view(128, heads=4)), 3), (dict(x=_view(128, s_n=132)), 4),
     (dict(x=_view(128, s_b=-64)), 1), (dict(x=_view(128, s_b=1 << 39)), 3),
@@ -140,7 +144,8 @@ def test_binding_refusals():
         with pytest.raises(ValueError, match=match):
             vsa.linear(x, w, **change)
     for change, match in [
-        (dict(dout=_fake(2, 8, 16)), "dout"), (dict(dout=_fake(2, 8, 24).float()), "dout"), (dict(activation="silu"), "z"),
+        (dict(dout=_fake(2, 8, 16)), "dout"), (dict(dout=_fake(2, 8, 24).float()), "dout"),
+        (dict(activation="silu"), "z"),
         (dict(activation="silu", z=_fake(2, 8, 16)), "z"), (dict(dx=_fake(2, 8, 24)), "dx"),
     ]:
         with pytest.raises(ValueError, match=match):

@@ -166,8 +166,8 @@ vsa_status encode(CUtensorMap* m, const RowsView& v, long long rows, long long b
   const cuuint64_t strides[3] = {rows > 1 ? (cuuint64_t)v.s_n * 2 : row, v.heads > 1 ? (cuuint64_t)v.s_h * 2 : row,
                                  batches > 1 ? (cuuint64_t)v.s_b * 2 : row};
   const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
-  return enc(m, type ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.data, dims, strides, box,
-             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUtensorMapDataType kind = type ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(m, kind, 4, v.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? VSA_OK
              : VSA_ERR_CUDA;
@@ -326,7 +326,8 @@ vsa_status vsa_linear(const vsa_linear_sizes* sizes, const vsa_heads* x, const v
   if (!known_activation(activation)) return VSA_ERR_UNSUPPORTED;
   e = check_view(x, sizes, sizes->K, false);
   if (e == VSA_OK) e = check_view(out, sizes, sizes->F, true);
-  if (e == VSA_OK && residual) e = residual->heads != out->heads ? VSA_ERR_SHAPE : check_view(residual, sizes, sizes->F, false);
+  if (e == VSA_OK && residual)
+    e = residual->heads != out->heads ? VSA_ERR_SHAPE : check_view(residual, sizes, sizes->F, false);
   if (e == VSA_OK && z) e = z->heads != out->heads ? VSA_ERR_SHAPE : check_view(z, sizes, sizes->F, true);
   if (e == VSA_OK) e = check_weight(weight, weight_stride, sizes);
   if (e != VSA_OK) return e;
@@ -373,7 +374,8 @@ vsa_status vsa_linear(const vsa_linear_sizes* sizes, const vsa_heads* x, const v
 
 size_t vsa_linear_backward_workspace_bytes(const vsa_linear_sizes* sizes, int activation) {
   int sms = 0;
-  if (check_sizes(sizes) != VSA_OK || !known_activation(activation) || vsa::current_device_sms(&sms) != VSA_OK) return 0;
+  if (check_sizes(sizes) != VSA_OK || !known_activation(activation)) return 0;
+  if (vsa::current_device_sms(&sms) != VSA_OK) return 0;
   if (!sizes->B || !sizes->N) return 0;
   return backward_bytes(sizes, activation, true, true, true, sms).total();
 }
@@ -412,7 +414,8 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
   z = single_token(z, swap, store + 1);
   dout = single_token(dout, swap, store + 2);
   dx = single_token(dx, swap, store + 3);
-  const BackwardBytes bytes = backward_bytes(sizes, activation, dx != nullptr, dweight != nullptr, dbias != nullptr, sms);
+  const BackwardBytes bytes =
+      backward_bytes(sizes, activation, dx != nullptr, dweight != nullptr, dbias != nullptr, sms);
   e = check_workspace(workspace, ws_bytes, bytes.total());
   if (e != VSA_OK) return e;
   uint8_t* const ws = static_cast<uint8_t*>(workspace);

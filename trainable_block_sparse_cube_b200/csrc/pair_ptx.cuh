@@ -1,5 +1,5 @@
 // Inline-PTX wrappers used by the linear product beyond those of
-// sm100_ptx.cuh: 4-D tiled copies and tcgen05 over a pair of CTAs
+// sm100_ptx.cuh: 4-D tiled loads and tcgen05 over a pair of CTAs
 // (cta_group::2). Written from the PTX ISA description of these instructions;
 // no load multicasts.
 #pragma once
@@ -23,8 +23,8 @@ __device__ __forceinline__ bool elect_one() {
 // Tiled 4-D load global -> this CTA's shared memory, completing on an mbarrier
 // (transaction bytes) at a shared::cluster address, which may be the other
 // CTA's of the pair.
-__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                            int c3) {
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3) {
   asm volatile(
       "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
       "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),

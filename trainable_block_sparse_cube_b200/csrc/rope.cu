@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
 // Backward of the norm with the rotation: x.in = x, x.dy = dy, x.out = dx, the
 // block's weight gradients to p.partial[block][tensor][D].
 template <typename T, int L, bool INTER>
-__global__ void __launch_bounds__(kThreads, kBackwardPerSm) norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBackwardPerSm)
+    norm_rope_backward_kernel(const __grid_constant__ RopeParams p) {
   constexpr int STAGES = kBackwardStages;
   extern __shared__ uint4 ring[];
   __shared__ RopePair pairs[kRopePairs];
@@ -701,8 +702,8 @@ cudaError_t launch_norm_rope_backward(RopeParams p, int type, float* dwq, float*
   const int grid = plan_units(p, num_sms, kBackwardPerSm, kBackwardAngles);
   cudaError_t e = launch_any(p, type, true, grid, st);
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  return launch_behind(norm_weight_grad_kernel, dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, st, (const float*)p.partial, grid,
-                       p.D, dwq, dwk);
+  return launch_behind(norm_weight_grad_kernel, dim3((p.D + 31) / 32, 2), dim3(32, 32), 0, st,
+                       (const float*)p.partial, grid, p.D, dwq, dwk);
 }
 
 }  // namespace vsa
