@@ -388,7 +388,8 @@ typedef struct {
   long long list_batch;
 } vsa_positions;
 
-/* Sizes shared by q and k: type is a vsa_type; D a multiple of 8, at most 256.
+/* Sizes shared by q and k: type is a vsa_type; D a multiple of 8, at most 256;
+ * B at most 2^20, N at most 2^30, B*N at most 2^33.
  * B, N or a tensor's heads may be 0 (nothing to do for it). */
 typedef struct {
   int type;
@@ -445,7 +446,8 @@ vsa_status vsa_qk_norm_rope_backward(const vsa_rope_sizes* sizes, const vsa_rota
  * is rows of heads * D channels, channel h * D + d first in head order. With
  * more than one head D is a multiple of 64. W is [F, K], its rows
  * weight_stride elements apart. K and F are multiples of 8; type is
- * VSA_TYPE_BF16 or VSA_TYPE_FP16, of every tensor but bias and dbias (fp32).
+ * VSA_TYPE_BF16 or VSA_TYPE_FP16, of every tensor but bias and dbias (fp32);
+ * B, K and F are at most 2^20, B*N at most 2^30.
  * Sums are fp32 and the results rounded once. B or N may be 0. */
 typedef struct {
   int type;

@@ -318,3 +318,43 @@ def test_other_stream_and_captured_graphs():
     torch.cuda.synchronize()
     for _, out in graphs:
         assert all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
+@pytest.mark.parametrize("inter", [True, False])
+def test_fp32_outputs_off_the_32_byte_boundary(inter):
+    """Rows that start on 16-byte boundaries only, in place and beside other channels, as whole sectors' rows do."""
+    rot = vsa.Rotation(96, (32, 32, 32), interleaved=inter)
+    x, g = _gen(1, 2, 3, 21, 96, dtype=torch.float32).cuda(), _gen(2, 2, 3, 21, 96, dtype=torch.float32).cuda()
+    w = torch.rand(96, device="cuda") + 0.5
+    ref = vsa.qk_norm_rope(x, None, w, None, rot, grid=(1, 3, 7))[0]
+    back = vsa.qk_norm_rope_backward(x, None, w, None, g, None, rot, grid=(1, 3, 7))
+    for start in (4, 8):
+        wide = torch.full((2, 21, 3, 108), 7.0, device="cuda")
+        v = wide[..., start:start + 96].transpose(1, 2)
+        v.copy_(x)
+        vsa.qk_norm_rope(v, None, w, None, rot, grid=(1, 3, 7), q_out=v)
+        assert torch.equal(v, ref)
+        v.copy_(g)
+        got = vsa.qk_norm_rope_backward(x, None, w, None, v, None, rot, grid=(1, 3, 7), dq=v)
+        assert torch.equal(v, back[0]) and torch.equal(got[2], back[2])
+        v.fill_(7.0)
+        assert (wide == 7.0).all()
+
+
+def test_positions_that_are_no_numbers_or_far():
+    rot = vsa.Rotation(64, (24, 20, 20), scale=(1.0, 7.0, 1.0))            # 7 radians: more than a turn a position
+    x = _gen(3, 1, 1, 6, 64, dtype=torch.float32).cuda()
+    p = torch.tensor([[0.25, -0.75, 1e-30], [-1e-30, 3.5, -2.5], [float("nan"), 1, 2], [1, float("inf"), 2],
+                      [1e6 + 0.5, -1e6, 3], [2.0 ** 23, 0.5, -0.5]], device="cuda")
+    y = vsa.rope(x, None, rot, positions=p)[0]
+    ang = po.angles(p[[0, 1, 4, 5]].double().cpu().numpy(), (24, 20, 20), scale=(1.0, 7.0, 1.0))
+    keep = x[:, :, [0, 1, 4, 5]]
+    _check(y[:, :, [0, 1, 4, 5]], _rot_batch(_np(keep), ang[None, None], True), _partner_abs(_np(keep), 64, True), 26,
+           "fractions")
+    assert torch.isnan(y[0, 0, 2, :24]).all() and torch.isfinite(y[0, 0, 2, 24:]).all()
+    assert torch.isnan(y[0, 0, 3, 24:44]).all() and torch.isfinite(y[0, 0, 3, :24]).all()
+    far = torch.tensor([[-2 ** 31, 2 ** 31 - 1, 0]] * 6, dtype=torch.int32, device="cuda")
+    ang = po.angles(far.double().cpu().numpy(), (24, 20, 20))
+    y = vsa.rope(x, None, vsa.Rotation(64, (24, 20, 20)), positions=far)[0]
+    # the frequency is a double: 2^-53 of 2^31 radians is 2^-22, 4 steps more of 2^-24
+    _check(y, _rot_batch(_np(x), ang[None, None], True), _partner_abs(_np(x), 64, True), 26 + 8, "far")

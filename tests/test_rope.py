@@ -119,6 +119,13 @@ def test_refusals(lib, fn, kw, code):
     assert _call(lib, fn, **kw) == code
 
 
+def test_refusals_of_sizes_beyond_the_limits(lib):
+    listed = vsa.Positions(list=1 << 20, list_type=0)
+    for sizes in (vsa.RopeSizes(0, 1, (1 << 30) + 1, 64), vsa.RopeSizes(0, 1 << 14, 1 << 20, 64),
+                  vsa.RopeSizes(0, (1 << 20) + 1, 1, 64)):
+        assert _call(lib, sizes=sizes, where=listed) == 3
+
+
 def test_refusals_of_missing_structs_and_bad_numbers(lib):
     s, r, w, h = vsa.RopeSizes(0, 2, 64, 64), vsa.Rotation(64, (24, 20, 20)).spec, vsa.Positions(4, 4, 4), _heads()
     assert lib.vsa_rope(None, r, w, h, None, h, None, None) == 1

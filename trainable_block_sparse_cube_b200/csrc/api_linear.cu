@@ -114,7 +114,9 @@ Product weight_product(const vsa_linear_sizes* s, bool join, bool wide) {
 
 bool few_rows(const vsa_linear_sizes* s) { return (long long)s->B * s->N <= vsa::kFewRows; }
 
+// Blocks along the rows. One for a few rows: it writes db itself and saves a launch.
 int slope_blocks(long long M, int F, int sms) {
+  if (M <= 64) return 1;
   const long long strips = ceil_div(F, 256), rows = ceil_div(M, 8), most = 8LL * sms / strips;
   return (int)(rows < most ? rows : most > 1 ? most : 1);
 }
@@ -278,7 +280,7 @@ BackwardBytes backward_bytes(const vsa_linear_sizes* s, int act, bool dx, bool d
   const long long M = (long long)s->B * s->N;
   BackwardBytes b{};
   if (act != VSA_ACT_NONE) b.dz = align_up((size_t)M * s->F * 2);
-  if (db) b.sums = align_up((size_t)slope_blocks(M, s->F, sms) * s->F * 4);
+  if (db && slope_blocks(M, s->F, sms) > 1) b.sums = align_up((size_t)slope_blocks(M, s->F, sms) * s->F * 4);
   for (bool join : {false, true}) {
     if (dx) {
       Product p = input_product(s, join);
@@ -426,12 +428,12 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
     s.dout = dz;
     if (act) s.z = rows_view(z, F);
     s.dz = ws;
-    s.partial = dbias ? reinterpret_cast<float*>(ws + bytes.dz) : nullptr;
+    s.blocks_y = slope_blocks((long long)sizes->B * sizes->N, F, sms);
+    s.partial = !dbias ? nullptr : s.blocks_y == 1 ? dbias : reinterpret_cast<float*>(ws + bytes.dz);
     s.act = activation;
     s.batches = sizes->B;
     s.rows = sizes->N;
     s.F = F;
-    s.blocks_y = slope_blocks((long long)sizes->B * sizes->N, F, sms);
     if (vsa::launch_linear_slope(s, sizes->type, dbias, st) != cudaSuccess) return VSA_ERR_CUDA;
     if (act) {
       dz = plain_rows(ws, sizes->N, F);

@@ -17,7 +17,7 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
   if (s->type < VSA_TYPE_BF16 || s->type > VSA_TYPE_FP32) return VSA_ERR_UNSUPPORTED;
   if (s->B < 0 || s->N < 0) return VSA_ERR_SHAPE;
   if (s->D < 8 || s->D > 256 || s->D % 8) return VSA_ERR_UNSUPPORTED;
-  if (s->B > (1 << 20)) return VSA_ERR_UNSUPPORTED;
+  if (s->B > (1 << 20) || s->N > (1 << 30) || (long long)s->B * s->N > (1LL << 33)) return VSA_ERR_UNSUPPORTED;
   if (r->rot < 0 || r->rot > s->D || r->rot % 2) return VSA_ERR_SHAPE;
   if (!r->interleaved && r->rot % 16) return VSA_ERR_UNSUPPORTED;
   if (r->axes < 1 || r->axes > VSA_ROPE_MAX_AXES) return VSA_ERR_UNSUPPORTED;

@@ -851,7 +851,7 @@ cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaS
   if (type) slope_kernel<__half><<<grid, block, 0, st>>>(p);
   else slope_kernel<__nv_bfloat16><<<grid, block, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !p.partial) return e;
+  if (e != cudaSuccess || !p.partial || p.blocks_y == 1) return e;
   return launch_behind(column_sum_kernel, dim3((p.F + 31) / 32), dim3(32, 32), 0, st, (const float*)p.partial,
                        p.blocks_y, p.F, db);
 }

@@ -268,7 +268,7 @@ struct FewRowsParams {
 struct SlopeParams {
   RowsView dout, z;
   void* dz;                 // [batches * rows, F], with an activation
-  float* partial;           // [blocks_y, F] column sums or null
+  float* partial;           // [blocks_y, F] column sums (db itself, if there is one) or null
   int act, batches, rows, F;
   int blocks_y;
 };
