@@ -32,6 +32,8 @@
 // order: no atomics, the same bits every time.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "launch.cuh"
 #include "packed.cuh"
 #include "sm100_ptx.cuh"
@@ -477,38 +479,44 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
         for (int k = 0; k < U; ++k) now[k] = feed.row(k);
         feed.next();
         feed.load(p, ROWS, me.lane_row, me.chunk);
-        F2 o[U / 2][8], r[U / 2];
+        // A step of few heads leaves out the pairs that are not there.
+        auto rows = [&](auto pairs_of) {
+          constexpr int P = decltype(pairs_of)::value;
+          F2 o[P][8], r[P];
 #pragma unroll
-        for (int k = 0; k < U / 2; ++k) {
-          F2 v[8];
-          unpack_pair(now[2 * k], now[2 * k + 1], v);
-          me.other(now[2 * k], now[2 * k + 1], v, full, o[k]);
+          for (int k = 0; k < P; ++k) {
+            F2 v[8];
+            unpack_pair(now[2 * k], now[2 * k + 1], v);
+            me.other(now[2 * k], now[2 * k + 1], v, full, o[k]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[k][i] = fma2(o[k][i], B[i], mul2(v[i], A[i]));
+            for (int i = 0; i < 8; ++i) o[k][i] = fma2(o[k][i], B[i], mul2(v[i], A[i]));
+            if (p.norm) {
+              r[k] = mul2(v[0], v[0]);
+#pragma unroll
+              for (int i = 1; i < 8; ++i) r[k] = fma2(v[i], v[i], r[k]);
+            }
+          }
           if (p.norm) {
-            r[k] = mul2(v[0], v[0]);
+            row_sums<L>(r);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) r[k] = fma2(v[i], v[i], r[k]);
+            for (int k = 0; k < P; ++k) {
+              const float2 m = split2(fma2(r[k], both(inv_d), both(p.eps)));
+              r[k] = pair2(rsqrtf(m.x), rsqrtf(m.y));
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[k][i] = mul2(o[k][i], r[k]);
+            }
           }
-        }
-        if (p.norm) {
-          row_sums<L>(r);
 #pragma unroll
-          for (int k = 0; k < U / 2; ++k) {
-            const float2 m = split2(fma2(r[k], both(inv_d), both(p.eps)));
-            r[k] = pair2(rsqrtf(m.x), rsqrtf(m.y));
+          for (int k = 0; k < 2 * P; ++k) {
+            float a[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[k][i] = mul2(o[k][i], r[k]);
+            for (int i = 0; i < 8; ++i) a[i] = k & 1 ? split2(o[k / 2][i]).y : split2(o[k / 2][i]).x;
+            if (live && h0 + k < heads) store8(dst, a, p.wide != 0);
+            dst += step;
           }
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          float a[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = k & 1 ? split2(o[k / 2][i]).y : split2(o[k / 2][i]).x;
-          if (live && h0 + k < heads) store8(dst, a, p.wide != 0);
-          dst += step;
-        }
+        };
+        if (U > 2 && heads - h0 <= 2) rows(std::integral_constant<int, 1>());
+        else rows(std::integral_constant<int, U / 2>());
       }
     }
   }
