@@ -433,6 +433,7 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
     s.act = activation;
     s.batches = sizes->B;
     s.rows = sizes->N;
+    s.by_rows = vsa::Divisor(sizes->N);
     s.F = F;
     if (vsa::launch_linear_slope(s, sizes->type, dbias, st) != cudaSuccess) return VSA_ERR_CUDA;
     if (act) {

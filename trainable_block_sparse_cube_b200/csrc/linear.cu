@@ -752,19 +752,34 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeParams p) {
     const T* const dsrc = at<T>(p.dout, 0, 0, c);
     const T* const zsrc = p.act != kActNone ? at<T>(p.z, 0, 0, c) : nullptr;
     T* const dst = static_cast<T*>(p.dz) + c;
-#pragma unroll 2
-    for (unsigned m = blockIdx.y * 8 + ty; m < M; m += gridDim.y * 8) {
-      const unsigned b = m / (unsigned)p.rows, n = m - b * (unsigned)p.rows;
-      float v[8];
-      unpack8<T>(*reinterpret_cast<const uint4*>(dsrc + b * p.dout.s_b + n * p.dout.s_n), v);
-      if (p.act != kActNone) {
-        float z[8];
-        unpack8<T>(*reinterpret_cast<const uint4*>(zsrc + b * p.z.s_b + n * p.z.s_n), z);
-        times_slope(v, z, p.act);
-        *reinterpret_cast<uint4*>(dst + (long long)m * p.F) = pack8<T>(v);
-      }
+    const unsigned step = gridDim.y * 8;
+    const bool act = p.act != kActNone;
+    // the rows two ahead are asked for before a row is worked on
+    uint4 nd[2], nz[2];
+    auto ask = [&](unsigned m, int slot) {
+      if (m >= M) return;
+      const unsigned b = p.batches > 1 ? p.by_rows(m) : 0, n = m - b * (unsigned)p.rows;
+      nd[slot] = *reinterpret_cast<const uint4*>(dsrc + b * p.dout.s_b + n * p.dout.s_n);
+      if (act) nz[slot] = *reinterpret_cast<const uint4*>(zsrc + b * p.z.s_b + n * p.z.s_n);
+    };
+    const unsigned m0 = blockIdx.y * 8 + ty;
+    ask(m0, 0);
+    ask(m0 + step, 1);
+    for (unsigned m = m0; m < M;) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      for (int slot = 0; slot < 2; ++slot, m += step) {
+        if (m >= M) break;
+        float v[8], z[8];
+        unpack8<T>(nd[slot], v);
+        if (act) unpack8<T>(nz[slot], z);
+        ask(m + 2 * step, slot);
+        if (act) {
+          times_slope(v, z, p.act);
+          *reinterpret_cast<uint4*>(dst + (long long)m * p.F) = pack8<T>(v);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
+      }
     }
   }
   if (!p.partial) return;

@@ -270,6 +270,7 @@ struct SlopeParams {
   void* dz;                 // [batches * rows, F], with an activation
   float* partial;           // [blocks_y, F] column sums (db itself, if there is one) or null
   int act, batches, rows, F;
+  Divisor by_rows;
   int blocks_y;
 };
 
