@@ -115,7 +115,8 @@ __device__ __forceinline__ float sigmoid(float v) { return rcp_approx(1.f + exp2
 // h = P(-|z|) = exp(-z^2 / 2) t q(t) with t = 1 / (1 + 0.3111 |z|): q is of
 // degree 7, fitted for this to the least relative error over |z| <= 20
 // (1.9e-7; 4.7e-7 as evaluated), so h keeps its accuracy far below 0, at a
-// quarter of the instructions of erfcf (16384 x 1536 x 6144: 340 -> 281 us).
+// quarter of the instructions of the complementary error function
+// (16384 x 1536 x 6144: 340 -> 281 us).
 __device__ __forceinline__ float normal_tail(float a, float* density) {
   const float t = rcp_approx(fmaf(0.3111269772052765f, a, 1.f));
   const float e = exp2_approx(-0.5f * kLog2e * (a * a));

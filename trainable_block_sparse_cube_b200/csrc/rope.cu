@@ -10,8 +10,8 @@
 //
 // r is recomputed from x, which the backward reads anyway, so nothing is
 // saved. Everything between the loads and the stores is fp32 and rounded
-// once. A whole position times the fraction of a turn that a pair makes for one,
-// in 64 bits, keeps just the fraction of a turn in the low 64 bits of the
+// once. A whole position times the fraction of a turn that a pair makes for
+// one, in 64 bits, keeps just the fraction of a turn in the low 64 bits of the
 // product: exact to 2^-32 of a turn for any position, where fp32 would have
 // lost 20 of its 24 bits at 10^6. The rest of an fp32 position adds its own
 // product.
@@ -21,11 +21,14 @@
 // a thread keeps one (token, 8 channels) place for all heads of its unit, so
 // an angle is computed once for 24 or 80 rows of it. Two heads at a time are
 // worked on as packed pairs of fp32 (half the instructions: the norm is near
-// the issue limit otherwise), while the loads of the next heads are in
-// flight. A unit is a tile of tokens by a group of heads; the grid
-// holds the blocks that fit on the GPU and each strides over the units, the
-// number of groups being the one whose longest block is shortest
-// (plan_units).
+// the issue limit otherwise), while the rows of the next heads, tensors and
+// units are on their way into shared memory (Feed: the norm's backward of
+// 16,384 tokens x 24 heads of 128 in bf16 took 82 us with one step's rows ahead
+// in registers, 62 with it). A unit is a tile of tokens by a group of heads;
+// the grid holds the blocks that fit on the GPU and each strides over the
+// units, the number of groups being the one whose longest block is shortest
+// (plan_units). 61,440 tokens x 24 heads with the norm: 133 us, 0.88 of the
+// copy rate; 76,800 x 80 backward: 547 us, 0.89.
 //
 // The weight gradients are summed per thread over its rows, per block through
 // shared memory, and over the blocks by a second kernel, always in the same
