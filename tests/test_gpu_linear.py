@@ -309,6 +309,45 @@ def test_other_stream_and_captured_graphs():
         assert all(torch.equal(a, b) for a, b in zip(ref, out))
 
 
+def test_a_product_behind_other_kinds_of_work():
+    """The kernels that start while the work before them still runs wait for it: a fill, a copy, a join of two
+    streams, another product; eagerly and captured."""
+    w1, w2 = _randn(1, 512, 512, dtype=torch.bfloat16, std=0.05), _randn(2, 512, 512, dtype=torch.bfloat16, std=0.05)
+    src = _randn(3, 1, 3000, 512, dtype=torch.bfloat16)
+    x, y = torch.zeros_like(src), torch.empty_like(src)
+    other = torch.cuda.Stream()
+
+    def work():
+        y.zero_()
+        now = torch.cuda.current_stream()
+        other.wait_stream(now)
+        with torch.cuda.stream(other):
+            x.copy_(src)
+        now.wait_stream(other)
+        a = vsa.linear(x, w1, out=y)                   # behind the join
+        b = vsa.linear(a, w2)                          # behind a product
+        x.zero_()                                      # behind a product that reads it no more
+        c = vsa.linear(b, w1, residual=x)              # behind a fill
+        return (b, c) + vsa.linear_backward(b, w1, c, want=(True, True))[:2]
+
+    ref = [t.clone() for t in work()]
+    assert torch.equal(ref[0], vsa.linear(vsa.linear(src, w1), w2))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for seed in (3, 4, 3):
+        src.copy_(_randn(seed, 1, 3000, 512, dtype=torch.bfloat16))
+        for t in out:
+            t.fill_(float("nan"))
+        graph.replay()
+        for _ in range(3):
+            eager = [t.clone() for t in work()]
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, out))
+    assert all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
 def test_products_on_several_streams_at_once():
     """Persistent pairs of CTAs of many products in flight together, each with a workspace of its own."""
     cases = [(_randn(i, 1, 200 + 90 * i, 1024, dtype=torch.bfloat16), _randn(9 + i, 520, 1024, dtype=torch.bfloat16))
@@ -327,6 +366,28 @@ def test_products_on_several_streams_at_once():
     for i, runs in enumerate(got):
         for y, dx, dw in runs:
             assert torch.equal(y, ref[i]) and torch.equal(dx, back[i][0]) and torch.equal(dw, back[i][1])
+
+
+def test_beside_the_attention_on_another_stream():
+    """Both take tensor memory and most of an SM; each waits for the other's blocks and gets its own result."""
+    T, H, W, h, D = 8, 16, 16, 4, 128
+    plan = vsa.Plan(1, h, T, H, W, D, topk=8)
+    q, k, v = (_randn(i, 1, h, T * H * W, D, dtype=torch.bfloat16) for i in range(3))
+    gate = torch.ones(1, h, T * H * W, device="cuda")
+    x, w = _randn(5, 1, 2000, 512, dtype=torch.bfloat16), _randn(6, 1024, 512, dtype=torch.bfloat16)
+    ref, y = plan.run(q, k, v, gate, gate)[0], vsa.linear(x, w)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            o = plan.run(q, k, v, gate, gate)[0]
+        with torch.cuda.stream(b):
+            got.append((o, vsa.linear(x, w), vsa.linear_backward(x, w, y)[1]))
+    torch.cuda.synchronize()
+    plan.check()
+    dw = vsa.linear_backward(x, w, y)[1]
+    assert all(torch.equal(o, ref) and torch.equal(z, y) and torch.equal(g, dw) for o, z, g in got)
 
 
 def test_gradients_match_differences():
