@@ -219,15 +219,17 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   g.rows = (int)p.rows;
   g.row_tiles = (int)ceil_div(p.rows, 256);
   g.F = (int)p.cols;
-  g.col_tiles = (int)ceil_div(p.cols, p.t.bn);
   g.kblocks = (int)p.kblocks;
   g.kblocks_batch = (int)p.kblocks_batch;
   g.bias = ep.bias;
   g.act = ep.act;
   g.stall = g_stall.load(std::memory_order_relaxed);
   g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
-  const long long units = p.t.whole + p.t.rest * p.t.splits;
+  const long long units = p.t.whole + p.t.rest * p.t.splits, col_tiles = ceil_div(p.cols, p.t.bn);
   if (units >= 1LL << 31) return VSA_ERR_UNSUPPORTED;
+  g.order = vsa::TileOrder(g.batches * g.row_tiles, (int)col_tiles);
+  g.by_row_tiles = vsa::Divisor(g.row_tiles);
+  if (p.t.rest) g.by_rest = vsa::Divisor((uint32_t)p.t.rest);
   g.whole = (int)p.t.whole;
   g.rest = (int)p.t.rest;
   g.splits = p.t.splits;
@@ -240,9 +242,8 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   f.rest = g.rest;
   f.splits = g.splits;
   f.bn = g.bn;
-  f.batches = g.batches;
   f.row_tiles = g.row_tiles;
-  f.col_tiles = g.col_tiles;
+  f.order = g.order;
   f.rows = g.rows;
   f.F = g.F;
   f.bias = ep.bias;

@@ -259,18 +259,17 @@ struct Waiter {
 };
 
 // Tiles in the order they run in. The pairs that run together take a block of
-// kGroup row tiles by the columns beside it, so that what they load from L2 is
+// kTileGroup row tiles by the columns beside it, so that what they load from L2 is
 // few rows of A and few of B (8192^3: 2.25 -> 1.10 GB from DRAM).
 // Every second block goes back over the columns, whose last rows of B are still
 // in L2 (16384 x 5120 x 5120 with a residual 952 -> 801 MB; 76800 rows of it,
 // which the power cap slows, 3282-3409 -> 3136-3244 us).
-constexpr int kGroup = 8;
-__device__ __forceinline__ void tile_place(int tile, int all_rows, int col_tiles, int* rt, int* ct) {
-  const int group = tile / (kGroup * col_tiles), in = tile - group * kGroup * col_tiles;
-  const int high = min(kGroup, all_rows - group * kGroup);
-  const int col = in / high;
-  *rt = group * kGroup + in - col * high;
-  *ct = group & 1 ? col_tiles - 1 - col : col;
+__device__ __forceinline__ void tile_place(const TileOrder& o, int tile, int* rt, int* ct) {
+  const int group = (int)o.by_block(tile), in = tile - group * o.block;
+  const int high = min(kTileGroup, o.rows - group * kTileGroup);
+  const int col = high == kTileGroup ? in / kTileGroup : in / high;
+  *rt = group * kTileGroup + in - col * high;
+  *ct = group & 1 ? o.cols - 1 - col : col;
 }
 
 // A work unit: a tile, or one part of the contraction of a tile of the last
@@ -283,11 +282,11 @@ struct Unit {
     steps(p, u, &k0, &k1);
     if (u >= p.whole) {
       part = u - p.whole;
-      t = p.whole + part % p.rest;
+      t = p.whole + part - (int)p.by_rest(part) * p.rest;
     }
     int rt, ct;
-    tile_place(t, p.batches * p.row_tiles, p.col_tiles, &rt, &ct);
-    batch = p.batches > 1 ? rt / p.row_tiles : 0;
+    tile_place(p.order, t, &rt, &ct);
+    batch = p.batches > 1 ? (int)p.by_row_tiles(rt) : 0;
     row0 = (rt - batch * p.row_tiles) * 256;
     col0 = ct * p.bn;
   }
@@ -295,7 +294,7 @@ struct Unit {
     *k0 = 0;
     *k1 = p.kblocks;
     if (u >= p.whole) {
-      const unsigned split = (u - p.whole) / p.rest;
+      const unsigned split = p.by_rest(u - p.whole);
       *k0 = (int)((unsigned)p.kblocks * split / p.splits);
       *k1 = (int)((unsigned)p.kblocks * (split + 1) / p.splits);
     }
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const FinishParams p) {
   const int groups = p.bn / 8, per_tile = 256 * groups;
   const int tile = blockIdx.x / (per_tile / 256), in = (blockIdx.x % (per_tile / 256)) * 256 + threadIdx.x;
   int rt, ct;
-  tile_place(p.first + tile, p.batches * p.row_tiles, p.col_tiles, &rt, &ct);
+  tile_place(p.order, p.first + tile, &rt, &ct);
   const int b = rt / p.row_tiles, r = in / groups, cc = (in - r * groups) * 8;
   const int n = (rt - b * p.row_tiles) * 256 + r, c = ct * p.bn + cc;
   if (n >= p.rows || c >= p.F) return;

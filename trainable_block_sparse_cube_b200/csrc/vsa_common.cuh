@@ -221,6 +221,15 @@ struct RowsView {
   long long s_b, s_h, s_n;
 };
 
+// The tiles' order: blocks of kTileGroup row tiles by all columns (see linear.cu).
+constexpr int kTileGroup = 8;
+struct TileOrder {
+  int rows = 0, cols = 0, block = 0;  // row tiles of all batches, column tiles, tiles of a block
+  Divisor by_block;
+  TileOrder() = default;
+  TileOrder(int r, int c) : rows(r), cols(c), block(kTileGroup * c), by_block(kTileGroup * c) {}
+};
+
 // out = A B^T on the tensor cores. A and B are 4-D maps (channel of a head,
 // row, head, batch) in 128-byte swizzle with boxes of 64 channels. A K-major operand is read along
 // its channels, an MN-major one along its rows.
@@ -236,7 +245,9 @@ struct GemmParams {
   int bn;                   // columns of a tile: a multiple of 32, 64 to 256
   int batches, row_tiles;   // batches x row_tiles tiles of 256 rows
   int rows;                 // rows of a batch
-  int F, col_tiles;         // columns
+  int F;                    // columns
+  TileOrder order;
+  Divisor by_row_tiles, by_rest;
   int kblocks;              // 64-long blocks of the contraction
   int kblocks_batch;        // kGemmWeight: blocks of a batch of rows
   int whole, rest, splits;  // tiles computed in one go, and those computed in parts of the contraction
@@ -250,7 +261,8 @@ struct GemmParams {
 // Sums the parts of the split tiles (number first, first + 1, ...) and applies the epilogue.
 struct FinishParams {
   const float* partial;     // [splits, rest, 256, bn]
-  int first, rest, splits, bn, batches, row_tiles, col_tiles, rows, F;
+  int first, rest, splits, bn, row_tiles, rows, F;
+  TileOrder order;
   const float* bias;
   int act;
   RowsView residual, z, out;   // data null: none
