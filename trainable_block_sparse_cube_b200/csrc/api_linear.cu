@@ -52,9 +52,10 @@ Tiling choose(long long batches, long long rows, long long cols, long long kbloc
       if (step < c) step = c;
     const double epilogue = 2000 + 25.0 * bn, all = kblocks * step;
     const double base = whole / pairs * ((all > epilogue ? all : epilogue) + 800) + epilogue;
-    for (int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-      if (s > 1 && (s > kblocks || rest * s > pairs || !rest)) break;
-      double cost = base + (rest ? ceil_div(kblocks, s) * step + 800 : 0);
+    const long long most = kblocks < 64 ? pairs : 4 * pairs;  // parts: a long contraction may take several rounds
+    for (int s : {1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 24, 32}) {
+      if (s > 1 && (s > kblocks || rest * s > most || !rest)) break;
+      double cost = base + ceil_div(rest * s, pairs) * (ceil_div(kblocks, s) * step + 800);
       if (s > 1) cost += 2500 + 8.0 * s * rest * tile_rows * bn / 2700;
       if (best_cost < 0 || cost < best_cost) {
         best_cost = cost;
