@@ -492,8 +492,9 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
 vsa_status vsa_linear_check(void* stream);
 
 /* Test hook, for all calls of the process: the limit of the linear product's
- * device-side waits (1 s by default), and whether its operands are left
- * unloaded so that the waits run out. */
+ * device-side waits (1 s by default), and whether they are made to run out:
+ * stall 1 leaves the operands unloaded, 2 loads half of them only after the
+ * wait for them ran out (or a second), 0 neither. */
 vsa_status vsa_linear_set_limits(uint64_t wait_ns, int stall);
 
 #ifdef __cplusplus

@@ -471,9 +471,10 @@ vsa_status vsa_linear_check(void* stream) {
 }
 
 vsa_status vsa_linear_set_limits(uint64_t wait_ns, int stall) {
-  if (!wait_ns) return VSA_ERR_INVALID_ARG;
-  g_wait_ns.store(wait_ns, std::memory_order_relaxed);
-  g_stall.store(stall != 0, std::memory_order_relaxed);
+  if (!wait_ns || stall < 0 || stall > vsa::kStallLate) return VSA_ERR_INVALID_ARG;
+  const uint64_t most = 1000000000000000;  // eleven days: multiples of it fit into 64 bits
+  g_wait_ns.store(wait_ns < most ? wait_ns : most, std::memory_order_relaxed);
+  g_stall.store(stall, std::memory_order_relaxed);
   return VSA_OK;
 }
 

@@ -50,6 +50,7 @@ struct Barriers {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drained;
   uint32_t tmem;
+  uint32_t stop;  // the loads stop before this step, counted over the pair's units; see Waiter::stage
 };
 constexpr int kGemmSmem = 1024 + kRingBytes + (int)sizeof(Barriers);
 static_assert(kGemmSmem <= 227 * 1024, "shared memory");
@@ -242,9 +243,34 @@ __device__ __forceinline__ T* at(const RowsView& v, int b, int n, int c) {
 }
 
 // ---------------------------------------------------------------- tensor cores
+// Limit of the waits for what is under way already: loads and MMAs that were issued.
+constexpr unsigned long long kDrainNs = 2000000000ull;
+
 // Bounded waits; a warp's lanes give up together.
 struct Waiter {
   unsigned long long limit;
+  // A loading warp's wait for a stage. While the pair's MMAs go on, the only
+  // other end is `stop`: the warp that issues them, whose waits have the limit,
+  // gives up at some step m and sets it to m + stages in both CTAs. The steps
+  // before that need nothing but MMAs that are under way, so both CTAs issue
+  // their loads of exactly these steps, for which that warp then waits: no
+  // load is in flight when the pair's shared memory goes. The time here is
+  // above all that the other warps may wait in between, and runs out in no
+  // other case.
+  __device__ __forceinline__ bool stage(uint64_t* bar, uint32_t parity, const uint32_t* stop, uint32_t step) const {
+    uint64_t t0 = 0;
+    for (int late = 0;;) {
+      bool done = false;
+#pragma unroll 1
+      for (int i = 0; i < 64 && !done; ++i) done = mbar_try_wait(bar, parity);
+      if (__all_sync(0xffffffffu, done)) return true;
+      if (__any_sync(0xffffffffu, step >= load_cluster(stop))) return false;
+      const uint64_t now = globaltimer_ns();
+      if (!t0) t0 = now;
+      late += now - t0 > 8 * limit + kDrainNs;
+      if (__any_sync(0xffffffffu, late > 4096)) return gave_up();
+    }
+  }
   // `seen`: what an earlier look at the barrier found.
   __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, bool seen = false) const {
     return __all_sync(0xffffffffu, seen) || __all_sync(0xffffffffu, mbar_wait(bar, parity, limit)) || gave_up();
@@ -334,6 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
     mbar_init(&sh.drained, 1);
+    sh.stop = ~0u;
     fence_mbar_init();
     prefetch_tmap(&p.ta);
     prefetch_tmap(&p.tb);
@@ -358,11 +385,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int b_boxes = (half + 63) / 64;
     const uint32_t b_bytes = KIND == kGemmForward ? half * 128 : b_boxes * 8192;
     const uint32_t full0 = mapa(smem_u32(&sh.full[0]), 0);
-    const bool load = p.stall == 0;
+    const bool load = p.stall != kStallUnloaded;
     Ring ring(p);
     // A look at the next barrier is taken before this step's work: its answer
     // is there when it is needed.
     bool ok = true, mine = warp == 0, seen = true;
+    uint32_t step = 0;  // of all units
     for (unsigned u = pair; ok && u < units; u += pairs) {
       // Divisions here; the steps keep their coordinates up by additions (a
       // division costs the issuing warp more than a load).
@@ -390,13 +418,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool load_a = KIND == kGemmWeight || row < p.rows;
       const uint32_t a_bytes = KIND == kGemmWeight ? kTileA : p.a_rows * 128;
       const uint32_t pair_bytes = 2 * b_bytes + (KIND == kGemmWeight || w.row0 + 128 < p.rows ? 2 : 1) * a_bytes;
-      for (int kb = w.k0; kb < w.k1; ++kb, ring.next()) {
+      for (int kb = w.k0; kb < w.k1; ++kb, ++step, ring.next()) {
         const int s = ring.stage;
         // passes at once where no use came before
         if (mine) {
-          if (!(ok = wait.warp(&sh.empty[s], ring.parity ^ 1, seen))) break;
+          ok = __all_sync(0xffffffffu, seen) || wait.stage(&sh.empty[s], ring.parity ^ 1, &sh.stop, step);
+          if (!ok) break;
           const Ring next = ring.after(2);
           seen = mbar_test(&sh.empty[next.stage], next.parity ^ 1);
+          if (p.stall == kStallLate && rank == 1 && step < 2) {  // test hook: until the MMAs are given up, or about 1 s
+            for (int i = 0; i < 1000000 && load_cluster(&sh.stop) == ~0u; ++i) __nanosleep(1000);
+            __syncwarp();
+          }
         }
         if (mine && elect_one()) {
           const uint32_t bar = full0 + s * 8;
@@ -424,9 +457,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (k >= kend) k = 0, ++kh;
       }
     }
-    if (!ok && rank == 0)  // the loads in flight land before the pair's shared memory goes
-      for (int i = 0; i < p.stages; ++i)
-        mbar_wait(&sh.full[i], i < ring.stage ? ring.parity : ring.parity ^ 1, p.wait_ns);
+    // the MMAs' last arrivals on these barriers, before the shared memory goes
+    for (int i = 0; ok && warp == 0 && i < p.stages; ++i, ++step, ring.next())
+      ok = wait.stage(&sh.empty[ring.stage], ring.parity ^ 1, &sh.stop, step);
   } else if (warp == 2) {
     if (rank == 0) {
       // ---- MMAs of the pair
@@ -438,6 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t bd0 = sdesc_sw128(base + p.tile_a, KIND == kGemmForward ? 16 : 8192, 1024);
       Ring ring(p);
       int tile = 0;
+      uint32_t step = 0;  // of all units
       bool ok = true, seen = false;
       for (unsigned u = pair; ok && u < units; u += pairs, ++tile) {
         int k0, k1;
@@ -448,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         uint32_t add = 0;
-        for (int kb = k0; kb < k1; ++kb, ring.next()) {
+        for (int kb = k0; kb < k1; ++kb, ++step, ring.next()) {
           const int s = ring.stage;
           ok = wait.warp(&sh.full[s], ring.parity, seen);
           if (!ok) break;
@@ -465,10 +499,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           add = 1;
         }
       }
-      if (!ok) {  // the MMAs in flight end before the tensor memory goes
-        if (elect_one()) mma_commit_pair(&sh.drained);
-        mbar_wait(&sh.drained, 0, p.wait_ns);
+      if (!ok) {  // the loads that both CTAs issue up to `stop` land
+        if (lane < 2) store_cluster(mapa(smem_u32(&sh.stop), lane), step + p.stages);
+        uint32_t all = 0;
+        for (unsigned u = pair; u < units; u += pairs) {
+          int k0, k1;
+          Unit::steps(p, u, &k0, &k1);
+          all += k1 - k0;
+        }
+        const uint32_t end = min(all, step + p.stages);
+        for (; p.stall != kStallUnloaded && step < end; ++step, ring.next())
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[ring.stage], ring.parity, kDrainNs))) break;
       }
+      // The MMAs end before the tensor memory goes, also where an epilogue gave up on them.
+      if (elect_one()) mma_commit_pair(&sh.drained);
+      mbar_wait(&sh.drained, 0, kDrainNs);
     }
   } else {
     // ---- epilogue: a warp takes 32 rows, a row a lane, and one half of the tile's
@@ -610,7 +655,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tmem, 512);
+  if (warp == 2) {
+    if (rank) mbar_wait(&sh.drained, 0, kDrainNs);  // committed before the barrier above
+    __syncwarp();
+    tmem_dealloc_pair(tmem, 512);
+  }
 }
 
 // ---------------------------------------------------------------- split contractions

@@ -230,6 +230,9 @@ struct TileOrder {
   TileOrder(int r, int c) : rows(r), cols(c), block(kTileGroup * c), by_block(kTileGroup * c) {}
 };
 
+// Test hook: operands are left unloaded, or the odd CTAs load theirs only after the wait for them ran out.
+enum : int { kStallUnloaded = 1, kStallLate = 2 };
+
 // out = A B^T on the tensor cores. A and B are 4-D maps (channel of a head,
 // row, head, batch) in 128-byte swizzle with boxes of 64 channels. A K-major operand is read along
 // its channels, an MN-major one along its rows.
@@ -253,7 +256,7 @@ struct GemmParams {
   int whole, rest, splits;  // tiles computed in one go, and those computed in parts of the contraction
   const float* bias;        // [F] or null
   int act;
-  int stall;                // test hook: no operand is loaded
+  int stall;                // test hook: kStall...
   unsigned long long wait_ns;
   long long units;          // whole + rest x splits
 };
