@@ -406,7 +406,7 @@ struct Feed {
           copy(dst, src + far, n);
           if (DY) copy(dst + U * PIECES * kThreads * 16, dsrc + far, n);
         }
-        if (there) {
+        if (k + 1 < left) {  // the last head's address stays for copies of nothing: it is inside and aligned
           src += step;
           if (DY) dsrc += dstep;
         }
