@@ -486,12 +486,16 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
                                const vsa_heads* dx, void* dweight, float* dbias, void* workspace, size_t ws_bytes,
                                void* stream);
 
-/* Synchronises `stream` and returns VSA_ERR_TIMEOUT if a wait inside a linear
- * product of the current device gave up since the last check (its results are
- * then invalid). Not while a graph is captured. */
+/* Synchronises `stream` (of the current device) and returns VSA_ERR_TIMEOUT if
+ * a wait inside a linear product that was enqueued on it gave up since its
+ * last check (the results are then invalid). No other stream's check takes
+ * this from it. Products captured into graphs are counted for the device: the
+ * next check of every stream tells of them. Beyond 255 streams of a device
+ * some are told of another's products too. VSA_ERR_CUDA, with nothing done,
+ * while the stream is being captured. */
 vsa_status vsa_linear_check(void* stream);
 
-/* Test hook, for all calls of the process: the limit of the linear product's
+/* Test hook, for the calls that this host thread makes: the limit of the linear product's
  * device-side waits (1 s by default), and whether they are made to run out:
  * stall 1 leaves the operands unloaded, 2 loads half of them only after the
  * wait for them ran out (or a second), 0 neither. */

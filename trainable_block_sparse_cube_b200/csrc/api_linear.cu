@@ -1,6 +1,8 @@
 // Host side of the linear product's entry points of include/vsa.h: argument
 // checks, the choice of tiles, tensor maps and launches.
-#include <atomic>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "host.cuh"
 #include "vsa_common.cuh"
@@ -9,8 +11,89 @@ namespace {
 
 using vsa::RowsView;
 
-std::atomic<unsigned long long> g_wait_ns{1000000000ull};
-std::atomic<int> g_stall{0};
+// vsa_linear_set_limits
+thread_local unsigned long long t_wait_ns = 1000000000ull;
+thread_local int t_stall = 0;
+
+// Which word counts the failures of a stream's products, and how many of them
+// its checks have told of. A product in a graph runs on streams that are not
+// known when it is captured: those count in word 0, of which every stream is
+// told. Streams beyond the number of words share theirs; each of them is then
+// told of all that it counts.
+class Failures {
+ public:
+  // The word for a product about to be enqueued on `st`.
+  unsigned word(cudaStream_t st) try {
+    Key key;
+    if (capturing(st) || !find(st, &key)) return 0;
+    std::lock_guard<std::mutex> lock(mutex_);
+    return entry(key).word;
+  } catch (...) {  // no host memory for the stream's entry
+    return 0;
+  }
+
+  // Whether products of `st` or of graphs failed since the last look.
+  vsa_status look(cudaStream_t st) try {
+    Key key;
+    if (capturing(st) || !find(st, &key)) return VSA_ERR_CUDA;
+    unsigned counts[vsa::kLinearFailureWords];
+    if (vsa::linear_failures(counts, st) != cudaSuccess) return VSA_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mutex_);
+    Entry& e = entry(key);
+    Device& d = devices_[key.first];
+    const bool own = news(counts[e.word], &e.told, &d.told[e.word]), graphs = news(counts[0], &e.told_graphs, &d.told[0]);
+    return own || graphs ? VSA_ERR_TIMEOUT : VSA_OK;
+  } catch (...) {
+    return VSA_ERR_CUDA;
+  }
+
+ private:
+  using Key = std::pair<int, unsigned long long>;  // device, the stream's number (never used again)
+  struct Entry {
+    unsigned word = 0, told = 0, told_graphs = 0;
+  };
+  struct Device {
+    unsigned streams = 0, told[vsa::kLinearFailureWords] = {};  // the highest counts that any stream was told
+  };
+
+  static bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {
+      cudaGetLastError();  // the legacy stream beside a capture
+      return true;
+    }
+    return s != cudaStreamCaptureStatusNone;
+  }
+  static bool find(cudaStream_t st, Key* key) {
+    return cudaGetDevice(&key->first) == cudaSuccess && cudaStreamGetId(st, &key->second) == cudaSuccess;
+  }
+  // A new stream is not told of what others were told before it came.
+  Entry& entry(const Key& key) {
+    auto [it, fresh] = entries_.try_emplace(key);
+    if (fresh) {
+      Device& d = devices_[key.first];
+      Entry& e = it->second;
+      e.word = 1 + d.streams++ % (vsa::kLinearFailureWords - 1);
+      e.told = d.told[e.word];
+      e.told_graphs = d.told[0];
+    }
+    return it->second;
+  }
+  static bool news(unsigned count, unsigned* told, unsigned* told_any) {
+    if ((int)(count - *told) <= 0) return false;  // counts may wrap around
+    *told = count;
+    if ((int)(count - *told_any) > 0) *told_any = count;
+    return true;
+  }
+
+  std::mutex mutex_;
+  std::map<Key, Entry> entries_;
+  std::map<int, Device> devices_;
+};
+Failures& failures() {
+  static Failures f;
+  return f;
+}
 
 inline size_t align_up(size_t x, size_t to = 256) { return (x + to - 1) / to * to; }
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -224,8 +307,9 @@ vsa_status run_product(const Product& p, int type, const RowsView& a, const Rows
   g.kblocks_batch = (int)p.kblocks_batch;
   g.bias = ep.bias;
   g.act = ep.act;
-  g.stall = g_stall.load(std::memory_order_relaxed);
-  g.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  g.stall = t_stall;
+  g.wait_ns = t_wait_ns;
+  g.failures = failures().word(st);
   const long long units = p.t.whole + p.t.rest * p.t.splits, col_tiles = ceil_div(p.cols, p.t.bn);
   if (units >= 1LL << 31) return VSA_ERR_UNSUPPORTED;
   g.order = vsa::TileOrder(g.batches * g.row_tiles, (int)col_tiles);
@@ -463,18 +547,16 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
 }
 
 vsa_status vsa_linear_check(void* stream) {
-  int sms = 0, word = 0;
-  vsa_status e = vsa::current_device_sms(&sms);
-  if (e != VSA_OK) return e;
-  if (vsa::linear_error_word(&word, static_cast<cudaStream_t>(stream)) != cudaSuccess) return VSA_ERR_CUDA;
-  return word ? VSA_ERR_TIMEOUT : VSA_OK;
+  int sms = 0;
+  const vsa_status e = vsa::current_device_sms(&sms);
+  return e == VSA_OK ? failures().look(static_cast<cudaStream_t>(stream)) : e;
 }
 
 vsa_status vsa_linear_set_limits(uint64_t wait_ns, int stall) {
   if (!wait_ns || stall < 0 || stall > vsa::kStallLate) return VSA_ERR_INVALID_ARG;
   const uint64_t most = 1000000000000000;  // eleven days: multiples of it fit into 64 bits
-  g_wait_ns.store(wait_ns < most ? wait_ns : most, std::memory_order_relaxed);
-  g_stall.store(stall, std::memory_order_relaxed);
+  t_wait_ns = wait_ns < most ? wait_ns : most;
+  t_stall = stall;
   return VSA_OK;
 }
 

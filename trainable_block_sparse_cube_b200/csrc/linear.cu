@@ -39,7 +39,11 @@ namespace {
 
 using namespace ptx;
 
-__device__ int g_linear_error;
+// How many warps gave up waiting, in the products of each stream that has a
+// word here. They only grow: a reader compares with what it saw before, so
+// that none can take a failure from another, and none is lost between a look
+// and a reset.
+__device__ unsigned g_linear_failures[kLinearFailureWords];
 
 constexpr int kRingBytes = 7 * 32768, kTileA = 16384;
 constexpr int kEpiWarps = 8, kThreads = 96 + 32 * kEpiWarps;  // two warps load, one issues MMAs
@@ -249,6 +253,7 @@ constexpr unsigned long long kDrainNs = 2000000000ull;
 // Bounded waits; a warp's lanes give up together.
 struct Waiter {
   unsigned long long limit;
+  unsigned word;  // of g_linear_failures
   // A loading warp's wait for a stage. While the pair's MMAs go on, the only
   // other end is `stop`: the warp that issues them, whose waits have the limit,
   // gives up at some step m and sets it to m + stages in both CTAs. The steps
@@ -278,8 +283,8 @@ struct Waiter {
   __device__ __forceinline__ bool pair(uint64_t* bar, uint32_t parity) const {  // arrivals of both CTAs
     return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit)) || gave_up();
   }
-  __device__ __forceinline__ static bool gave_up() {
-    atomicOr(&g_linear_error, kErrTimeout);
+  __device__ __forceinline__ bool gave_up() const {
+    atomicAdd(&g_linear_failures[word], 1u);
     return false;
   }
 };
@@ -354,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const unsigned pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, units = (unsigned)p.units;
   const int half = p.bn / 2;  // rows of B in a CTA
-  const Waiter wait{p.wait_ns};
+  const Waiter wait{p.wait_ns, p.failures};
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < p.stages; ++s) mbar_init(&sh.full[s], 1), mbar_init(&sh.empty[s], 1);
@@ -924,13 +929,9 @@ cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaS
                        p.blocks_y, p.F, db);
 }
 
-cudaError_t linear_error_word(int* word, cudaStream_t st) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_linear_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  static const int zero = 0;
-  if (e == cudaSuccess && *word)
-    e = cudaMemcpyToSymbolAsync(g_linear_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-  return e;
+cudaError_t linear_failures(unsigned (&counts)[kLinearFailureWords], cudaStream_t st) {
+  const cudaError_t e = cudaMemcpyFromSymbolAsync(counts, g_linear_failures, sizeof(counts), 0, cudaMemcpyDeviceToHost, st);
+  return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
 }  // namespace vsa

@@ -258,6 +258,7 @@ struct GemmParams {
   int act;
   int stall;                // test hook: kStall...
   unsigned long long wait_ns;
+  unsigned failures;        // word that counts waits that ran out
   long long units;          // whole + rest x splits
 };
 
@@ -297,8 +298,10 @@ cudaError_t launch_linear_gemm(const GemmParams& p, int kind, int type, int num_
 cudaError_t launch_linear_finish(const FinishParams& p, int type, cudaStream_t st);
 cudaError_t launch_linear_few_rows(const FewRowsParams& p, int type, cudaStream_t st);
 cudaError_t launch_linear_slope(const SlopeParams& p, int type, float* db, cudaStream_t st);
-// Reads and clears the current device's error word of the linear kernels (synchronises the stream).
-cudaError_t linear_error_word(int* word, cudaStream_t st);
+// The current device's counts of waits that ran out in linear products: word 0
+// those captured into graphs, the others those of streams (synchronises `st`).
+constexpr int kLinearFailureWords = 256;
+cudaError_t linear_failures(unsigned (&counts)[kLinearFailureWords], cudaStream_t st);
 
 cudaError_t launch_gather(const GatherParams& p, int D, int num_sms, cudaStream_t st);
 cudaError_t launch_coarse(const CoarseParams& p, cudaStream_t st);

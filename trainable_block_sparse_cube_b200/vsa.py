@@ -755,7 +755,7 @@ def linear_backward(x, weight, dout, z=None, activation=None, bias=False, dx=Non
 
 
 def linear_check(device=None):
-    """Synchronises the current stream of the device and raises VSAError if a wait inside a linear product on it
-    gave up since the last check."""
+    """Synchronises the current stream of the device and raises VSAError if a wait inside a linear product that was
+    enqueued on it, or captured into a graph, gave up since this stream's last check. Not while it is captured."""
     with torch.cuda.device(device):
         _check(load().vsa_linear_check(_stream()), "vsa_linear_check")
