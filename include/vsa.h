@@ -365,8 +365,11 @@ typedef struct {
  * pair j of them turns by pos[axis[j]] * freq[j] radians,
  *   (u, v) -> (u cos - v sin, u sin + v cos).
  * Pair j is channels (2j, 2j + 1) if interleaved, else (j, j + rot/2), and
- * then rot is a multiple of 16. Angles are exact to 2^-32 of a turn at any
- * position, so far positions lose nothing. */
+ * then rot is a multiple of 16. |freq| is below 2^64. Angles are within 2^-31
+ * of a turn of the product at every int32 position and grid, so far positions
+ * lose nothing. An fp32 position counts to 2^-32 and its angle is within 2^-30
+ * of a turn up to 2^31; one of size p beyond that adds p 2^-64 of a turn, and
+ * from 2^63 on, or if it is no number, the channels that turn with it are NaN. */
 typedef struct {
   int rot, interleaved;
   int axes; /* 1 .. VSA_ROPE_MAX_AXES */

@@ -1,4 +1,6 @@
 """Calls of the projection side that its documentation allows at the edges of their arguments."""
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -59,3 +61,53 @@ def test_strides_of_dimensions_of_length_one(dtype, shape, stride):
         g = _randn(11, B, N, 72, dtype=dtype)
         got, ref = (vsa.linear_backward(x, weight, d, bias=True) for x, d in ((odd[0], _odd(g, stride)), (q, g)))
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def _pi():
+    """pi to 400 bits: 16 arctan(1/5) - 4 arctan(1/239)."""
+    one = 1 << 420
+
+    def arctan(x):
+        term, total, n = one // x, 0, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+
+    return Fraction(16 * arctan(5) - 4 * arctan(239), one)
+
+
+@pytest.mark.parametrize("kind", [torch.int32, torch.float32], ids=str)
+@pytest.mark.parametrize("scale", [(1.0, -0.5, 7.0), (1000.0, -1000.0, 2.0 ** 40), (2.0 ** 60, -3e-9, 0.3)], ids=str)
+def test_angles_of_far_positions(scale, kind):
+    """Against the product position x frequency (a double) with pi to 400 bits. The bound on y is that of the other
+    tests of the rotation: 26 steps of 2^-24 of |x_u| + |x_v| and the rounding; fp32 positions are whole numbers here,
+    below 2^31."""
+    D, sections = 64, (24, 20, 20)
+    rot = vsa.Rotation(D, sections, scale=scale)
+    top = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 128, -2 ** 31 + 128, 10 ** 6 + 1, -(10 ** 8) - 7, 1, 0]
+    p = torch.tensor(top).to(kind)[:, None].expand(-1, 3).contiguous()
+    p[:, 1] = p[:, 1].roll(1)
+    if kind is torch.float32:
+        p = p.clamp(-2.0 ** 31 + 128, 2.0 ** 31 - 128)
+    x = _randn(3, 1, 2, len(top), D, dtype=torch.float32)
+    y = vsa.rope(x, None, rot, positions=p.cuda())[0].double().cpu()
+    pi = _pi()
+    turn = [[float(2 * pi * (Fraction(int(p[n, rot.spec.axis[j]])) * Fraction(rot.spec.freq[j]) / (2 * pi) % 1))
+             for j in range(D // 2)] for n in range(len(top))]
+    a = torch.tensor(turn, dtype=torch.float64)
+    u, v = x.double().cpu()[..., 0::2], x.double().cpu()[..., 1::2]
+    ref = torch.stack([u * a.cos() - v * a.sin(), u * a.sin() + v * a.cos()], -1).flatten(-2)
+    size = (u.abs() + v.abs()).repeat_interleave(2, -1)
+    assert ((y - ref).abs() <= 26 * 2.0 ** -24 * size + 2.0 ** -24 * ref.abs()).all()
+
+
+def test_fp32_positions_beyond_the_range_are_nan():
+    rot = vsa.Rotation(64, (24, 20, 20))
+    x = _randn(3, 1, 1, 3, 64, dtype=torch.float32)
+    p = torch.tensor([[2.0 ** 63, 0, 0], [0, -2.0 ** 63, 0], [0, 0, 3e38]], device="cuda")
+    y = vsa.rope(x, None, rot, positions=p)[0][0, 0]
+    for n, (a, b) in enumerate(((0, 24), (24, 44), (44, 64))):
+        assert torch.isnan(y[n, a:b]).all()
+        assert torch.equal(y[n, :a], x[0, 0, n, :a]) and torch.equal(y[n, b:], x[0, 0, n, b:])

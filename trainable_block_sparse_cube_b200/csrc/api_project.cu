@@ -1,6 +1,7 @@
 // Host side of the projection-side entry points of include/vsa.h (rotary
 // positions, per-head norm): argument checks and launches. They hold no state.
 #include <cmath>
+#include <cstring>
 
 #include "host.cuh"
 #include "vsa_common.cuh"
@@ -10,6 +11,35 @@ namespace {
 using vsa::check_heads;
 
 static_assert(vsa::kRopePairs == VSA_ROPE_MAX_PAIRS && vsa::kRopeAxes == VSA_ROPE_MAX_AXES, "ABI limits");
+
+// Radians a position -> turns a position, modulo 2^32, to the nearest 2^-64:
+// the frequency's 53 bits times 192 bits of 1 / (2 pi), in whole numbers. Both
+// a quotient of doubles and its fraction would be off by 2^-53 of themselves,
+// which positions near 2^31 make 2^-22 of a turn, and fast ones more.
+vsa::RopePair turns_of(double freq, int axis) {
+  static constexpr uint64_t kInverse[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+  uint64_t f;
+  std::memcpy(&f, &freq, 8);
+  const int e = (int)(f >> 52 & 0x7ff);  // |freq| = m 2^(e - 1075), e at least 1 there
+  const uint64_t m = (f & ((1ull << 52) - 1)) | (uint64_t)(e > 0) << 52;
+  uint64_t digits[4], carry = 0;  // of the product, in 2^(e - 1075 - 192)
+  for (int i = 0; i < 3; ++i) {
+    const unsigned __int128 p = (unsigned __int128)kInverse[i] * m + carry;
+    digits[i] = (uint64_t)p;
+    carry = (uint64_t)(p >> 64);
+  }
+  digits[3] = carry;
+  const int drop = 192 - 64 + 1075 - (e > 0 ? e : 1);  // 117 at least, as frequencies stay below 2^64
+  const auto bits = [&](int i) -> uint64_t {  // 64 of them from the i-th on
+    const int w = i / 64, s = i % 64;
+    return w > 3 ? 0 : digits[w] >> s | (s && w < 3 ? digits[w + 1] << (64 - s) : 0);
+  };
+  uint64_t low = bits(drop), high = bits(drop + 64);
+  const uint64_t up = bits(drop - 1) & 1;
+  low += up, high += up && !low;
+  if (freq < 0) low = 0 - low, high = ~high + (low == 0);
+  return vsa::RopePair{(uint32_t)low, (uint32_t)(low >> 32), (uint32_t)high, axis};
+}
 
 // The parts of RopeParams that every call shares.
 vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation* r, const vsa_positions* o) {
@@ -29,12 +59,8 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
   p->interleaved = r->interleaved != 0;
   p->axes = r->axes;
   for (int j = 0; j < r->rot / 2; ++j) {
-    if (r->axis[j] < 0 || r->axis[j] >= r->axes || !std::isfinite(r->freq[j])) return VSA_ERR_INVALID_ARG;
-    const double turns = r->freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double whole = std::floor(turns), fraction = turns - whole;
-    const uint64_t bits = fraction < 1.0 ? (uint64_t)(fraction * 18446744073709551616.0) : 0;  // 2^64
-    const double around = whole - 4294967296.0 * std::floor(whole / 4294967296.0);             // modulo 2^32
-    p->pairs[j] = vsa::RopePair{(uint32_t)bits, (uint32_t)(bits >> 32), (uint32_t)(uint64_t)around, r->axis[j]};
+    if (r->axis[j] < 0 || r->axis[j] >= r->axes || !(std::fabs(r->freq[j]) < 0x1p64)) return VSA_ERR_INVALID_ARG;
+    p->pairs[j] = turns_of(r->freq[j], r->axis[j]);
   }
   if (!o->list) {
     if (r->axes != 3 || o->T < 1 || o->H < 1 || o->W < 1) return VSA_ERR_SHAPE;

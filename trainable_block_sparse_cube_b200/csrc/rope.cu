@@ -12,9 +12,9 @@
 // saved. Everything between the loads and the stores is fp32 and rounded
 // once. A whole position times the fraction of a turn that a pair makes for
 // one, in 64 bits, keeps just the fraction of a turn in the low 64 bits of the
-// product: exact to 2^-32 of a turn for any position, where fp32 would have
-// lost 20 of its 24 bits at 10^6. The rest of an fp32 position adds its own
-// product.
+// product: within 2^-31 of a turn for positions up to 2^31, where fp32 would
+// have lost 20 of its 24 bits at 10^6. The rest of an fp32 position, in 2^-32,
+// adds its own product.
 //
 // Bound by HBM: a row is read once and written once (the norm's backward
 // reads x and dy). A lane moves 8 channels, a power of two of lanes a row, and
@@ -161,7 +161,7 @@ __device__ __forceinline__ void row_sums(F2 (&v)[N]) {
 struct Positions {
   uint32_t low[kRopeAxes], rest[kRopeAxes];
   int high[kRopeAxes];
-  float bad[kRopeAxes];  // NaN for a position that is not finite, else 0
+  float bad[kRopeAxes];  // NaN for a position that is no number or not below 2^63 in size, else 0
 
   __device__ __forceinline__ void whole(int a, long long v) {
     low[a] = (uint32_t)v;
@@ -185,7 +185,7 @@ struct Positions {
           const float v = there ? static_cast<const float*>(p.pos)[o + a] : 0.f, f = floorf(v);
           whole(a, (long long)f);
           rest[a] = (uint32_t)((v - f) * 4294967296.f);
-          bad[a] = v - v;
+          bad[a] = fabsf(v) < 0x1p63f ? 0.f : __int_as_float(0x7fc00000);
         }
       }
     }
