@@ -111,3 +111,42 @@ def test_fp32_positions_beyond_the_range_are_nan():
     for n, (a, b) in enumerate(((0, 24), (24, 44), (44, 64))):
         assert torch.isnan(y[n, a:b]).all()
         assert torch.equal(y[n, :a], x[0, 0, n, :a]) and torch.equal(y[n, b:], x[0, 0, n, b:])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_and_values_of_every_finite_z(act, dtype):
+    """act and act' at every finite number of the type, through products with one term (exact): y = act(z) and
+    dx = act'(z). Bound: 32 + 16 |z| + 4 z^2 + |z|^3 steps of 2^-24 of a value's terms (see the linear product's
+    tests) and half a step of the type; results below 2^-126 may be 0. Where |z| > 13 act is z or 0 and act' 1 or 0 to
+    the last bit that counts."""
+    top = 2 ** 16
+    bits = torch.arange(top, dtype=torch.int32, device="cuda").to(torch.int16)
+    z = bits.view(dtype)
+    z = z[torch.isfinite(z)]
+    n = z.numel() // 8 * 8
+    z = z[:n]
+    x = torch.zeros(1, 40, 8, dtype=dtype, device="cuda")                     # rows of 1: x W^T is W's first column
+    x[:, :, 0] = 1
+    w = torch.zeros(n, 8, dtype=dtype, device="cuda")
+    w[:, 0] = z
+    y = vsa.linear(x, w, activation=act)[0, 0]
+    dout = torch.ones(1, n // 8, 8, dtype=dtype, device="cuda")
+    eye = torch.eye(8, dtype=dtype, device="cuda")
+    slope = vsa.linear_backward(torch.zeros(1, n // 8, 8, dtype=dtype, device="cuda"), eye, dout,
+                                z=z.view(1, n // 8, 8), activation=act, want=(True, False))[0].flatten()
+    t = z.double()
+    if act == "gelu":
+        p = 0.5 * torch.special.erfc(-t * 0.5 ** 0.5)
+        ref, ds = t * p, t * torch.exp(-0.5 * t * t) / (2 * torch.pi) ** 0.5
+    else:
+        a, b = (1.0, 0.0) if act == "silu" else (2 * (2 / torch.pi) ** 0.5, 2 * (2 / torch.pi) ** 0.5 * 0.044715)
+        far = t.clamp(-1e4, 1e4)                                              # 0 and 1 beyond, in 64 bits too
+        p = torch.sigmoid(far * (a + b * far * far))
+        ref, ds = t * p, far * p * torch.sigmoid(-far * (a + b * far * far)) * (a + 3 * b * far * far)
+    m = t.abs().clamp(max=1e4)
+    steps = (32 + 16 * m + 4 * m ** 2 + m ** 3).clamp(max=2.0 ** 20) * 2.0 ** -24
+    half, tiny = torch.finfo(dtype).eps / 2, 2.0 ** -25 if dtype is torch.float16 else 2.0 ** -126 * 128
+    assert torch.isfinite(y).all() and torch.isfinite(slope).all()
+    assert ((y.double() - ref).abs() <= (steps + half) * 1.01 * ref.abs() + tiny).all()
+    assert ((slope.double() - p - ds).abs() <= steps * 2 * (p.abs() + ds.abs()) + half * 1.01 * (p + ds).abs() + tiny).all()

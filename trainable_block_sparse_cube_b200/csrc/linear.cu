@@ -156,8 +156,9 @@ __device__ __forceinline__ float slope(float z) {
     return fmaf(z * s, 1.f - s, s);
   }
   if (ACT == kActGeluTanh) {
-    const float s = sigmoid(z * fmaf(kTanhB, z * z, kTanhA));
-    return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z * z, kTanhA), s);
+    const float z2 = fminf(z * z, 1e30f);  // a finite z far out meets no 0 x infinity; NaN comes from z itself
+    const float s = sigmoid(z * fmaf(kTanhB, z2, kTanhA));
+    return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z2, kTanhA), s);
   }
   if (ACT == kActGelu) {  // P(z) + z exp(-z^2 / 2) / sqrt(2 pi)
     float e;
