@@ -150,3 +150,22 @@ def test_slopes_and_values_of_every_finite_z(act, dtype):
     assert torch.isfinite(y).all() and torch.isfinite(slope).all()
     assert ((y.double() - ref).abs() <= (steps + half) * 1.01 * ref.abs() + tiny).all()
     assert ((slope.double() - p - ds).abs() <= steps * 2 * (p.abs() + ds.abs()) + half * 1.01 * (p + ds).abs() + tiny).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")], ids=str)
+def test_a_weight_that_is_no_number_stays_in_its_channel(bad, interleaved):
+    """Channels 48 to 63 are not rotated: y = x w r there, each for itself."""
+    rot = vsa.Rotation(64, (16, 16, 16), interleaved=interleaved)
+    q = _randn(1, 1, 3, 20, 64, dtype=torch.float32)
+    w = 1 + 0.2 * _randn(2, 64, dtype=torch.float32)
+    ref = vsa.qk_norm_rope(q, None, w, None, rot, grid=(1, 4, 5))[0]
+    for c in (48, 55, 63):
+        wb = w.clone()
+        wb[c] = bad
+        y = vsa.qk_norm_rope(q, None, wb, None, rot, grid=(1, 4, 5))[0]
+        rest = [i for i in range(64) if i != c]
+        assert torch.equal(y[..., rest], ref[..., rest])
+        want = q[..., c] * bad
+        assert torch.equal(torch.isnan(y[..., c]), torch.isnan(want))
+        assert torch.isnan(want).all() or torch.equal(y[..., c], want)

@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm) rope_kernel(const __g
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           A[i] = both(me.c[i] * x.w[me.chunk * 8 + i]);
-          B[i] = both(me.s[i] * x.w[pc * 8 + (INTER ? i ^ 1 : i)]);
+          // a channel that is not rotated has no partner, whose weight may be no number
+          if (me.turned >> i & 1u) B[i] = both(me.s[i] * x.w[pc * 8 + (INTER ? i ^ 1 : i)]);
         }
       }
 #pragma unroll 1
