@@ -378,7 +378,7 @@ typedef struct {
 } vsa_rotation;
 
 /* Positions of the tokens.
- *   list == NULL: the raster grid, N = T*H*W, axes = 3, token (t, h, w) at
+ *   list == NULL: the raster grid, N = T*H*W (0 if one of them is), axes = 3, token (t, h, w) at
  *     origin + (t, h, w) (an image has T = 1; a later frame of a video that is
  *     generated frame by frame has T = 1 and its number in origin[0]).
  *   list != NULL: device array [B, N, axes] of int32 (list_type 0) or fp32

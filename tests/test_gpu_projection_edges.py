@@ -169,3 +169,15 @@ def test_a_weight_that_is_no_number_stays_in_its_channel(bad, interleaved):
         want = q[..., c] * bad
         assert torch.equal(torch.isnan(y[..., c]), torch.isnan(want))
         assert torch.isnan(want).all() or torch.equal(y[..., c], want)
+
+
+def test_a_grid_without_tokens():
+    rot = vsa.Rotation(64, (24, 20, 20))
+    q, k = _randn(1, 2, 3, 0, 64), _randn(2, 2, 1, 0, 64)
+    w = torch.ones(64, device="cuda")
+    for grid in ((0, 4, 4), (2, 0, 3), (2, 3, 0)):
+        kw = dict(grid=grid)
+        for out in (vsa.rope(q, k, rot, **kw), vsa.rope_backward(q, k, rot, **kw), vsa.qk_norm_rope(q, k, w, w, rot, **kw)):
+            assert [t.shape for t in out] == [q.shape, k.shape]
+        dq, dk, dwq, dwk = vsa.qk_norm_rope_backward(q, k, w, w, q, k, rot, **kw)
+        assert dq.shape == q.shape and dk.shape == k.shape and not dwq.any() and not dwk.any()

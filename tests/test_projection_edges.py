@@ -31,3 +31,10 @@ def test_refusals_of_frequencies(lib, freq):
     assert _rope(lib, rot=rot) == 1
     rot.freq[3] = 2.0 ** 63
     assert _rope(lib, N=0, rot=rot, positions=vsa.Positions(list=1 << 20)) == 0
+
+
+@pytest.mark.parametrize("T,H,W", [(0, 4, 4), (2, 0, 3), (2, 3, 0), (0, 0, 0)])
+def test_a_grid_without_tokens(lib, T, H, W):
+    assert _rope(lib, N=0, T=T, H=H, W=W) == 0
+    assert _rope(lib, N=1, T=T, H=H, W=W) == 2
+    assert _rope(lib, N=0, T=T, H=H, W=-1) == 2

@@ -63,9 +63,9 @@ vsa_status fill(vsa::RopeParams* p, const vsa_rope_sizes* s, const vsa_rotation*
     p->pairs[j] = turns_of(r->freq[j], r->axis[j]);
   }
   if (!o->list) {
-    if (r->axes != 3 || o->T < 1 || o->H < 1 || o->W < 1) return VSA_ERR_SHAPE;
-    // each product stays below 2^62: no overflow
-    const long long hw = (long long)o->H * o->W;
+    if (r->axes != 3 || o->T < 0 || o->H < 0 || o->W < 0) return VSA_ERR_SHAPE;
+    const long long hw = (long long)o->H * o->W;  // each product stays below 2^62: no overflow
+    if (!hw || !o->T) return s->N ? VSA_ERR_SHAPE : VSA_OK;
     if (s->N % hw || s->N / hw != o->T) return VSA_ERR_SHAPE;
     p->pos_kind = 0;
     p->H = o->H;
