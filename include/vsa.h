@@ -482,7 +482,8 @@ size_t vsa_linear_backward_workspace_bytes(const vsa_linear_sizes* sizes, int ac
  *   dx = dz W,  dweight [F, K] = dz^T x,  dbias [F] (fp32) = sum of dz over rows;
  * the residual's gradient is dout. Any of dx, dweight and dbias may be NULL. x
  * is read for dweight, the weight for dx, z (as many heads as dout) with an
- * activation. dz is rounded to the type before its products, not for dbias.
+ * activation; act' is 0 and 1 at an infinite z, which a sum can become when z is
+ * rounded to fp16. dz is rounded to the type before its products, not for dbias.
  * Sums run in a fixed order. */
 vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x, const void* weight,
                                long long weight_stride, const vsa_heads* z, int activation, const vsa_heads* dout,

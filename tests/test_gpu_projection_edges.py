@@ -181,3 +181,29 @@ def test_a_grid_without_tokens():
             assert [t.shape for t in out] == [q.shape, k.shape]
         dq, dk, dwq, dwk = vsa.qk_norm_rope_backward(q, k, w, w, q, k, rot, **kw)
         assert dq.shape == q.shape and dk.shape == k.shape and not dwq.any() and not dwk.any()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_at_an_infinite_z(act):
+    """Sums of -4e5 and 4e5 are infinite once rounded to fp16, but act of the first is 0 and its slope 0."""
+    x = torch.zeros(1, 40, 8, dtype=torch.float16, device="cuda")
+    x[:, :, 0] = 1000
+    w = torch.zeros(16, 8, dtype=torch.float16, device="cuda")
+    w[:, 0] = torch.tensor([-400.0, 400.0, 0.001, -0.5] * 4)
+    z = torch.empty(1, 40, 16, dtype=torch.float16, device="cuda")
+    y = vsa.linear(x, w, activation=act, z=z)
+    assert (z[..., 0::4] == float("-inf")).all() and (z[..., 1::4] == float("inf")).all()
+    assert (y[..., 0::4] == 0).all() and torch.isfinite(y[..., 2::4]).all()
+    g = torch.ones_like(z)
+    dx, dw, db = vsa.linear_backward(x, w, g, z=z, activation=act, bias=True)
+    assert (db[0::4] == 0).all() and (db[1::4] == 40).all() and torch.isfinite(db).all()
+    assert torch.isfinite(dw[0::4]).all() and torch.isfinite(dx).all()
+    for dtype in (torch.float16, torch.bfloat16):
+        far = torch.tensor([float("-inf"), float("inf"), float("nan"), 0.0] * 2, dtype=dtype, device="cuda")
+        far = far.expand(1, 70, 8).contiguous()
+        db = vsa.linear_backward(far, torch.eye(8, dtype=dtype, device="cuda"), torch.ones_like(far), z=far, activation=act,
+                                 bias=True, want=(False, False))[2]
+        assert torch.equal(db[:2], torch.tensor([0.0, 70.0], device="cuda")) and torch.isnan(db[2])
+        # at 0 all three slopes are 1/2, gelu's by a tail that is right to 5.2e-7 of 1/2 up to |z| = 1 and two
+        # operations more: below 32 steps of 2^-24, the bound of the other tests of slopes, in each of 70 terms of 1/2
+        assert abs(db[3] - 35) <= 70 * 0.5 * 32 * 2.0 ** -24

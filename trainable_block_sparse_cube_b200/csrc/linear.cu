@@ -149,16 +149,25 @@ __device__ __forceinline__ float activate(float z) {
   return z;
 }
 
+// Slopes are 0 or 1 long before 1e19, whose square is finite: beyond it, and at
+// the infinity that a sum becomes when it is rounded to fp16, z would meet
+// factors of 0. A NaN stays one.
+__device__ __forceinline__ float within(float z) {
+  float v;
+  asm("min.NaN.f32 %0, %1, 0f5F0AC723;\n\tmax.NaN.f32 %0, %0, 0fDF0AC723;" : "=&f"(v) : "f"(z));
+  return v;
+}
+
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
+  if (ACT != kActNone) z = within(z);
   if (ACT == kActSilu) {
     const float s = sigmoid(z);
     return fmaf(z * s, 1.f - s, s);
   }
   if (ACT == kActGeluTanh) {
-    const float z2 = fminf(z * z, 1e30f);  // a finite z far out meets no 0 x infinity; NaN comes from z itself
-    const float s = sigmoid(z * fmaf(kTanhB, z2, kTanhA));
-    return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z2, kTanhA), s);
+    const float s = sigmoid(z * fmaf(kTanhB, z * z, kTanhA));
+    return fmaf(z * s * (1.f - s), fmaf(3.f * kTanhB, z * z, kTanhA), s);
   }
   if (ACT == kActGelu) {  // P(z) + z exp(-z^2 / 2) / sqrt(2 pi)
     float e;
