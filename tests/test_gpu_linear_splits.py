@@ -41,7 +41,7 @@ def cut(batches, rows, cols, blocks, wide=False, pairs=74):
         tail = 2000 + 25.0 * bn
         base = tiles // pairs * (max(blocks * step, tail) + 800) + tail
         for s in (1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 24, 32):
-            if s > 1 and (s > blocks or rest * s > (pairs if blocks < 64 else 4 * pairs) or not rest):
+            if s > 1 and (s > blocks or rest * s > (pairs if cols <= bn else 4 * pairs) or not rest):
                 break
             cost = base + _up(rest * s, pairs) * (_up(blocks, s) * step + 800)
             if s > 1:
@@ -74,9 +74,10 @@ def _workspaces(B, N, K, F):
 CASES = [
     # B, N, K, F, heads in, heads out, activation, bias, residual, layout; cuts of forward, dx, dW
     ((1, 19003, 512, 64, 8, 0, "gelu", True, True, "heads"), "split+whole", "whole", None),
-    ((1, 10001, 6144, 64, 0, 0, "silu", True, True, "slice"), "split+rounds", "whole", None),
+    ((1, 10001, 6144, 64, 0, 0, "silu", True, True, "slice"), "whole", "whole", None),    # one column of tiles
+    ((1, 5003, 12288, 320, 0, 0, "silu", True, True, "slice"), "split+rounds", None, None),
     ((1, 19003, 64, 512, 0, 8, "gelu_tanh", True, False, "heads"), "whole", "split+whole", None),
-    ((1, 10001, 64, 6144, 0, 48, None, True, True, "heads"), None, "split+rounds", None),
+    ((1, 5003, 320, 12288, 0, 192, None, True, True, "heads"), None, "split+rounds", None),
     ((3, 6399, 512, 64, 8, 0, None, True, True, "heads"), "split+whole", None, None),     # batches that are no run
     ((1, 4099, 4096, 1536, 32, 12, "silu", True, False, "heads"), None, None, "split+whole"),
     ((1, 16001, 6144, 384, 48, 0, None, True, False, "heads"), None, None, "split+rounds"),

@@ -117,7 +117,12 @@ struct Tiling {
 // A round costs its steps, or the epilogue of the tile before, and the start of
 // a tile. The last round's tiles are too few for all pairs and are split along
 // the contraction, which costs a second kernel that reads the parts (40 x 4096
-// x 4096: 64 tiles of 64 columns 17.3 us, 22 of 192 in three parts 13.8).
+// x 4096: 64 tiles of 64 columns 17.3 us, 22 of 192 in three parts 13.8). The
+// parts may take several rounds where there is more than one column of tiles
+// (products with sides drawn from 64 to 7000 and contractions from 10,000 to
+// 40,000, where the cost picks that: 29 of them took 0.91 of the time of the
+// best cut into one round, 0.70 to 1.09; with one column of tiles 11 took 1.11,
+// 1.03 to 1.19).
 // `wide` allows only tiles whose second half of columns does not start inside
 // a head.
 Tiling choose(long long batches, long long rows, long long cols, long long kblocks, int sms, bool wide) {
@@ -135,7 +140,7 @@ Tiling choose(long long batches, long long rows, long long cols, long long kbloc
       if (step < c) step = c;
     const double epilogue = 2000 + 25.0 * bn, all = kblocks * step;
     const double base = whole / pairs * ((all > epilogue ? all : epilogue) + 800) + epilogue;
-    const long long most = kblocks < 64 ? pairs : 4 * pairs;  // parts: a long contraction may take several rounds
+    const long long most = cols <= bn ? pairs : 4 * pairs;  // parts
     for (int s : {1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 24, 32}) {
       if (s > 1 && (s > kblocks || rest * s > most || !rest)) break;
       double cost = base + ceil_div(rest * s, pairs) * (ceil_div(kblocks, s) * step + 800);
