@@ -273,6 +273,10 @@ struct Waiter {
   // above all that the other warps may wait in between, and runs out in no
   // other case.
   __device__ __forceinline__ bool stage(uint64_t* bar, uint32_t parity, const uint32_t* stop, uint32_t step) const {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || stage_loop(bar, parity, stop, step);
+  }
+  // Out of line: the code that every launch fetches anew stays short.
+  __device__ __noinline__ bool stage_loop(uint64_t* bar, uint32_t parity, const uint32_t* stop, uint32_t step) const {
     uint64_t t0 = 0;
     for (int late = 0;;) {
       bool done = false;
@@ -356,6 +360,22 @@ struct Ring {
     return r;
   }
 };
+
+// The end of the warp that issues the MMAs, when it gives up at `step`: the
+// loads that both CTAs issue up to `stop` land. Out of line, as it hardly runs.
+__device__ __noinline__ void give_up(const GemmParams& p, Barriers& sh, Ring ring, uint32_t step) {
+  const int lane = threadIdx.x & 31;
+  if (lane < 2) store_cluster(mapa(smem_u32(&sh.stop), lane), step + p.stages);
+  uint32_t all = 0;
+  for (unsigned u = blockIdx.x >> 1; u < (unsigned)p.units; u += gridDim.x >> 1) {
+    int k0, k1;
+    Unit::steps(p, u, &k0, &k1);
+    all += k1 - k0;
+  }
+  const uint32_t end = min(all, step + p.stages);
+  for (; p.stall != kStallUnloaded && step < end; ++step, ring.next())
+    if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[ring.stage], ring.parity, kDrainNs))) break;
+}
 
 // KIND kGemmForward: A and B K-major. kGemmInput: A K-major, B MN-major.
 // kGemmWeight: both MN-major, the contraction running over batches of rows.
@@ -472,9 +492,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (k >= kend) k = 0, ++kh;
       }
     }
-    // the MMAs' last arrivals on these barriers, before the shared memory goes
-    for (int i = 0; ok && warp == 0 && i < p.stages; ++i, ++step, ring.next())
-      ok = wait.stage(&sh.empty[ring.stage], ring.parity ^ 1, &sh.stop, step);
+    // The MMAs' last arrivals on these barriers come before the shared memory
+    // goes; stages that no step used have none.
+    if (ok && warp == 0) {
+      const int used = min(p.stages, (int)step);
+      for (int i = used; i < p.stages; ++i) ring.next();
+      for (int i = 0; ok && i < used; ++i, ring.next())
+        ok = wait.stage(&sh.empty[ring.stage], ring.parity ^ 1, &sh.stop, step + p.stages - used + i);
+    }
   } else if (warp == 2) {
     if (rank == 0) {
       // ---- MMAs of the pair
@@ -514,18 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           add = 1;
         }
       }
-      if (!ok) {  // the loads that both CTAs issue up to `stop` land
-        if (lane < 2) store_cluster(mapa(smem_u32(&sh.stop), lane), step + p.stages);
-        uint32_t all = 0;
-        for (unsigned u = pair; u < units; u += pairs) {
-          int k0, k1;
-          Unit::steps(p, u, &k0, &k1);
-          all += k1 - k0;
-        }
-        const uint32_t end = min(all, step + p.stages);
-        for (; p.stall != kStallUnloaded && step < end; ++step, ring.next())
-          if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[ring.stage], ring.parity, kDrainNs))) break;
-      }
+      if (!ok) give_up(p, sh, ring, step);
       // The MMAs end before the tensor memory goes, also where an epilogue gave up on them.
       if (elect_one()) mma_commit_pair(&sh.drained);
       mbar_wait(&sh.drained, 0, kDrainNs);
