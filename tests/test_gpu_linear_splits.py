@@ -110,3 +110,9 @@ def test_cuts(case, forward, dx, dw):
         assert (a.double() - ref).square().mean().sqrt() <= 2.0 ** -8 * ref.square().mean().sqrt()
         worst_row = ((a.double() - ref).square().mean(-1) / ref.square().mean(-1)).sqrt().max()
         assert worst_row <= 2.0 ** -7
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 17, 32])
+@pytest.mark.parametrize("K,F", [(1016, 4096), (1024, 4096), (1032, 4104), (2048, 4104), (2056, 4104)])
+def test_few_rows_by_either_number_of_warps(M, K, F):
+    tl.test_forward((1, M, K, F, 0, 0, "gelu_tanh", True, True, "rows"), torch.float16)

@@ -909,13 +909,18 @@ cudaError_t launch_gemm_kind(const GemmParams& p, int kind, int num_sms, cudaStr
   return launch_gemm<kGemmWeight, T>(p, num_sms, st);
 }
 
-// Long rows take sixteen warps a block, which keeps more of W in flight; for
-// short ones the joining of the warps' sums would cost more (one row: 1536 x
-// 9216 7.2 us with eight and 8.8 with sixteen, 4096 x 4096 11.4 and 8.7).
+// Sixteen warps a block keep more of W in flight, but fewer blocks fit on an SM
+// and more sums are joined. They are taken for rows longer than 2048, and from
+// 1024 on where the blocks are few or the rows many (us with eight and sixteen
+// warps, W out of memory; one row: 256 -> 4096 3.1 and 3.3, 1024 -> 4096 5.1 and
+// 4.4, 1536 -> 1536 5.6 and 4.3, 1536 -> 9216 8.3 and 9.5, 2048 -> 8192 9.6 and
+// 11.5, 4096 -> 4096 12.4 and 9.7, 4096 -> 12288 28.8 and 21.5; 16 rows:
+// 1536 -> 6144 7.7 and 9.6; 32 rows: 256 -> 9216 7.1 and 8.1, 1536 -> 9216 20.7
+// and 14.7).
 template <int NT, typename T>
 cudaError_t launch_few_tiles(const FewRowsParams& p, cudaStream_t st) {
   const int blocks = (p.F + kFewColumns - 1) / kFewColumns;
-  if (p.K > 2048) few_rows_kernel<NT, 16, T><<<blocks, 512, 0, st>>>(p);
+  if (p.K > 2048 || (p.K >= 1024 && (NT > 2 || blocks <= 256))) few_rows_kernel<NT, 16, T><<<blocks, 512, 0, st>>>(p);
   else few_rows_kernel<NT, 8, T><<<blocks, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
