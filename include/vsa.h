@@ -378,8 +378,8 @@ typedef struct {
 } vsa_rotation;
 
 /* Positions of the tokens.
- *   list == NULL: the raster grid, N = T*H*W (0 if one of them is), axes = 3, token (t, h, w) at
- *     origin + (t, h, w) (an image has T = 1; a later frame of a video that is
+ *   list == NULL: the raster grid, N = T*H*W (0 if one of them is), axes = 3,
+ *     token (t, h, w) at origin + (t, h, w) (an image has T = 1; a later frame of a video that is
  *     generated frame by frame has T = 1 and its number in origin[0]).
  *   list != NULL: device array [B, N, axes] of int32 (list_type 0) or fp32
  *     (list_type 1), batches list_batch elements apart (0: one list for all). */
@@ -484,7 +484,8 @@ size_t vsa_linear_backward_workspace_bytes(const vsa_linear_sizes* sizes, int ac
  * is read for dweight, the weight for dx, z (as many heads as dout) with an
  * activation; act' is 0 and 1 at an infinite z, which a sum can become when z is
  * rounded to fp16. dz is rounded to the type before its products, not for dbias.
- * Sums run in a fixed order. */
+ * Sums run in a fixed order. dx, dweight and dbias overlap one another and the
+ * inputs nowhere, the workspace included, which is used by one call at a time. */
 vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x, const void* weight,
                                long long weight_stride, const vsa_heads* z, int activation, const vsa_heads* dout,
                                const vsa_heads* dx, void* dweight, float* dbias, void* workspace, size_t ws_bytes,

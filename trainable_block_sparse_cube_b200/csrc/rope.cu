@@ -27,8 +27,8 @@
 // in registers, 62 with it). A unit is a tile of tokens by a group of heads;
 // the grid holds the blocks that fit on the GPU and each strides over the
 // units, the number of groups being the one whose longest block is shortest
-// (plan_units). 61,440 tokens x 24 heads with the norm: 133 us, 0.88 of the
-// copy rate; 76,800 x 80 backward: 547 us, 0.89.
+// (plan_units). 61,440 tokens x 24 heads with the norm: 130 to 139 us, 0.84 to
+// 0.90 of the copy rate; 76,800 x 80 backward: 546 us, 0.89.
 //
 // The weight gradients are summed per thread over its rows, per block through
 // shared memory, and over the blocks by a second kernel, always in the same

@@ -569,7 +569,8 @@ def rope(q, k, rotation, grid=None, origin=(0, 0, 0), positions=None, q_out=None
     """Rotary positions with several axes on q and k ([B, heads, N, D], any strides; k may be None or have
     another number of heads). Tokens lie on the raster ``grid`` (T, H, W) from ``origin`` on, or at
     ``positions`` ([N, axes] or [B, N, axes], int32 or float32). Returns (q_out, k_out), contiguous unless
-    given; an output may be its input. Enqueued on the current stream."""
+    given; an output may be its input. Enqueued on the current stream. Like every call here it leaves no trace for
+    autograd, also where an input requires a gradient: rope_backward gives it."""
     B, N, _, sizes, hq, hk = _sizes(q, k, rotation)
     device = q.device
     where = _where(rotation, grid, origin, positions, B, N, device)
@@ -694,7 +695,7 @@ def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out
     [F, K]; bias [F] fp32; activation None, "silu", "gelu" or "gelu_tanh". Returns [B, N, F], or
     [B, heads, N, F / heads] if ``heads`` is given; ``residual``, ``out`` and ``z`` (which receives
     x weight^T + bias for linear_backward) have that shape. out may be the residual. Enqueued on the current
-    stream."""
+    stream. The result has no autograd history, whatever x and weight require: linear_backward gives the gradients."""
     B, N, F, sizes, hx = _linear_sizes(x, weight, activation)
     device, dtype = x.device, x.dtype
     if bias is not None:
@@ -726,8 +727,8 @@ def linear(x, weight, bias=None, activation=None, residual=None, heads=None, out
 def linear_backward(x, weight, dout, z=None, activation=None, bias=False, dx=None, want=(True, True)):
     """Gradients of linear from that of its output (whose shape dout has): (dx, dweight, dbias). z is what linear
     stored, needed with an activation; dbias (fp32) is None unless ``bias``; ``want`` switches dx and dweight
-    off. dx is in the order of dimensions that x is stored in unless given. The residual's gradient is dout.
-    Enqueued on the current stream."""
+    off. dx is in the order of dimensions that x is stored in unless given; it overlaps no other argument. The
+    residual's gradient is dout. Enqueued on the current stream."""
     B, N, F, sizes, hx = _linear_sizes(x, weight, activation)
     device, dtype = x.device, x.dtype
     hg = _need_rows(dout, "dout", dtype, device)
