@@ -379,8 +379,9 @@ typedef struct {
 
 /* Positions of the tokens.
  *   list == NULL: the raster grid, N = T*H*W (0 if one of them is), axes = 3,
- *     token (t, h, w) at origin + (t, h, w) (an image has T = 1; a later frame of a video that is
- *     generated frame by frame has T = 1 and its number in origin[0]).
+ *     token (t, h, w) at origin + (t, h, w) (an image has T = 1; a later frame
+ *     of a video that is generated frame by frame has T = 1 and its number in
+ *     origin[0]).
  *   list != NULL: device array [B, N, axes] of int32 (list_type 0) or fp32
  *     (list_type 1), batches list_batch elements apart (0: one list for all). */
 typedef struct {
@@ -500,10 +501,10 @@ vsa_status vsa_linear_backward(const vsa_linear_sizes* sizes, const vsa_heads* x
  * while the stream is being captured. */
 vsa_status vsa_linear_check(void* stream);
 
-/* Test hook, for the calls that this host thread makes: the limit of the linear product's
- * device-side waits (1 s by default), and whether they are made to run out:
- * stall 1 leaves the operands unloaded, 2 loads half of them only after the
- * wait for them ran out (or a second), 0 neither. */
+/* Test hook, for the calls that this host thread makes: the limit of the
+ * linear product's device-side waits (1 s by default), and whether they are
+ * made to run out: stall 1 leaves the operands unloaded, 2 loads half of them
+ * only after the wait for them ran out (or a second), 0 neither. */
 vsa_status vsa_linear_set_limits(uint64_t wait_ns, int stall);
 
 #ifdef __cplusplus

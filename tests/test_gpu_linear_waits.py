@@ -175,3 +175,31 @@ def test_many_streams():
             _stalled(lambda: vsa.linear(x, w), limit=1)
     assert [_told(st) for st in streams] == [i % 2 == 0 for i in range(len(streams))]
     assert not any(_told(st) for st in streams) and not _told()
+
+
+@pytest.mark.parametrize("mode", ["global", "thread_local"])
+def test_products_of_one_thread_beside_a_capture_of_another(mode):
+    """The look at a stream's number and state spares the other thread's capture."""
+    x, w = _randn(1, 1, 300, 64), _randn(2, 256, 64)                       # no workspace: nothing is allocated meanwhile
+    ref = vsa.linear(x, w)
+    out, st, w2 = torch.empty_like(ref), torch.cuda.Stream(), _randn(3, 64, 256)
+    torch.cuda.synchronize()
+
+    def other():
+        with torch.cuda.stream(st):
+            for _ in range(3):
+                vsa.linear(x, w, out=out)
+
+    with ThreadPoolExecutor(1) as pool:
+        pool.submit(other).result()
+        torch.cuda.synchronize()
+        out.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, capture_error_mode=mode):
+            y = vsa.linear(x, w)
+            pool.submit(other).result()
+            y = vsa.linear(y, w2)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
+    g.replay()
+    assert torch.equal(y, vsa.linear(ref, w2)) and not _told() and not _told(st)

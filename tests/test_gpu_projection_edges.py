@@ -1,4 +1,5 @@
 """Calls of the projection side that its documentation allows at the edges of their arguments."""
+from concurrent.futures import ThreadPoolExecutor
 from fractions import Fraction
 
 import pytest
@@ -207,3 +208,34 @@ def test_slopes_at_an_infinite_z(act):
         # at 0 all three slopes are 1/2, gelu's by a tail that is right to 5.2e-7 of 1/2 up to |z| = 1 and two
         # operations more: below 32 steps of 2^-24, the bound of the other tests of slopes, in each of 70 terms of 1/2
         assert abs(db[3] - 35) <= 70 * 0.5 * 32 * 2.0 ** -24
+
+
+def test_first_calls_of_a_host_thread():
+    """A thread whose first use of the GPU is one of the library's calls has no context of its own yet; outputs that
+    are there already leave nothing else to make it one."""
+    x, w = _randn(1, 1, 300, 64), _randn(2, 256, 64)
+    dy, y, dx = _randn(3, 1, 300, 256), torch.empty(1, 300, 256, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x)
+    h = _randn(4, 1, 3, 300, 64)
+    o, rot = torch.empty_like(h), vsa.Rotation(64, (24, 20, 20))
+    plan = vsa.Plan(1, 1, 4, 8, 8, 64, topk=2)
+    q, k, v = (_randn(i, 1, 1, 256, 64) for i in (5, 6, 7))
+    gate = torch.ones(1, 1, 256, device="cuda")
+    outs = [t.clone() for t in plan.run(q, k, v, gate, gate)]
+    calls = [
+        (lambda: vsa.linear(x, w, out=y), [y], [vsa.linear(x, w)]),
+        (lambda: vsa.linear_backward(x, w, dy, dx=dx, want=(True, False)), [dx],
+         [vsa.linear_backward(x, w, dy, want=(True, False))[0]]),
+        (lambda: vsa.linear_backward(x, w, dy, want=(False, True)), [], []),
+        (lambda: vsa.rope(h, None, rot, grid=(3, 10, 10), q_out=o), [o], [vsa.rope(h, None, rot, grid=(3, 10, 10))[0]]),
+        (lambda: vsa.linear_check(), [], []),
+        (lambda: plan.run(q, k, v, gate, gate, *outs), outs, [t.clone() for t in outs]),
+    ]
+    for call, got, ref in calls:
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        with ThreadPoolExecutor(1) as pool:
+            pool.submit(call).result()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    plan.check()

@@ -25,6 +25,11 @@ inline EncodeTiledFn get_encode_fn() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
+  // The encoder fails in a host thread without a current context, which one
+  // that has made no call of the runtime before is; cudaSetDevice makes it so.
+  thread_local bool bound = false;
+  int dev = 0;
+  if (!bound) bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
   return fn;
 }
 
